@@ -403,6 +403,167 @@ sz_status sz_select_codebook(const uint32_t *d_hist256, uint8_t *d_codebook16, u
 sz_status sz_select_codebook_batched(uint32_t n_hists, const uint32_t *d_hists, uint8_t *d_codebooks,
                                      uint64_t *d_escapes_or_null, void *stream);
 
+/* ---------------------------------- the cache written and read in place */
+/*
+ * The two operators around the codec: sz_append_kv writes a layer's new keys
+ * and values into the paged cache that the batched calls encode, and
+ * sz_paged_attention reads that cache -- on the prefill side as it was
+ * written, on the decode side as sz_decode_batched rebuilt it (explainer,
+ * section 1 "Le probleme": the prefill team writes the notes, the decode
+ * team reads them).  Both take one token per request or long chunks, ragged
+ * over the requests, and neither has a gradient.
+ *
+ * sz_paged_kv -- one layer's cache and the requests of one call.
+ *   d_k, d_v        page pools of 16-bit values, 16-byte aligned.  Value
+ *                   (page p, head h, token t, channel c) is element
+ *                   p*stride[0] + h*stride[1] + t*stride[2] + c: any order of
+ *                   pages, heads and tokens, K and V in one pool or in two.
+ *                   Strides are multiples of 8 and nest without overlap (a
+ *                   dimension of size 1 may have any stride).  A page whose
+ *                   head, token and channel lie end to end is a page of
+ *                   heads*page_tokens*head_dim elements of the batched calls.
+ *   n_pages         pages in each pool
+ *   heads           KV heads
+ *   head_dim        channels per head: a multiple of 8, at most 256
+ *   page_tokens     tokens per page
+ *   dtype           SZ_BF16 or SZ_FP16 (of the pools and of q, k, v and out)
+ *   d_page_table    int32: request r's i-th page is page
+ *                   d_page_table[r*table_stride + i], i < max_pages.  Entries
+ *                   behind a request's last token are not read.
+ *   d_q_begin       int32[n_reqs + 1]: request r's new tokens are rows
+ *                   d_q_begin[r] .. d_q_begin[r+1] of q, k, v and out
+ *                   (ascending, the last at most n_tokens).  Rows outside
+ *                   every request are left alone.
+ *   d_kv_len        int32[n_reqs]: tokens cached once the new ones are in;
+ *                   new token i of n sits at position kv_len - n + i
+ *   n_tokens        rows of q, k, v and out
+ * The lengths live on the device, so a captured call serves other lengths of
+ * the same n_reqs, n_tokens and max_pages when the arrays change.
+ * d_status (required) gets one status per request: SZ_ERR_INVALID for rows
+ * out of order or out of range, a negative length or a page number outside
+ * the pool, SZ_ERR_CAPACITY for a kv_len above max_pages*page_tokens.  The
+ * results of a request whose status is not SZ_OK must not be used; nothing
+ * outside the caller's buffers is touched for it.
+ */
+#define SZ_BF16 1u
+#define SZ_FP16 2u
+
+typedef struct sz_paged_kv {
+    void *d_k;
+    void *d_v;
+    uint64_t k_stride[3]; /* elements between pages, heads, tokens */
+    uint64_t v_stride[3];
+    uint64_t n_pages;
+    uint32_t heads;
+    uint32_t head_dim;
+    uint32_t page_tokens;
+    uint32_t dtype;
+    const int32_t *d_page_table;
+    uint64_t table_stride;
+    const int32_t *d_q_begin;
+    const int32_t *d_kv_len;
+    uint32_t n_reqs;
+    uint32_t max_pages;
+    uint64_t n_tokens;
+} sz_paged_kv;
+
+/*
+ * sz_append_kv -- write the new tokens' keys and values into their pages,
+ * one launch: keys normalised per head and rotated by their position on the
+ * way, queries the same way into d_q_out, values as they are, and the
+ * exponents of what went into the cache counted for the codec.
+ *   d_k, d_v        new rows; element (token, head, c) is token*stride[0] +
+ *                   head*stride[1] + c, strides multiples of 8, 16-byte
+ *                   aligned
+ *   d_q_or_null, d_q_out, q_heads  queries (optional); d_q_out may be d_q
+ *                   with the same strides
+ *   d_q_norm_or_null, d_k_norm_or_null  dtype[head_dim] weights w of the
+ *                   norm y = x * w / sqrt(mean(x*x) + eps) over a head's
+ *                   channels; NULL: no norm
+ *   d_freqs_or_null double[rot_dim/2], radians per position of each rotated
+ *                   pair; NULL (with rot_dim 0): no rotation.  A long-context
+ *                   scaling is a choice of these.
+ *   rot_dim         channels rotated, the first of each head: a multiple of
+ *                   16, at most head_dim.  Pair t is channels (t, t +
+ *                   rot_dim/2), or (2t, 2t+1) if interleaved.
+ *   rot_scale       factor on the rotated channels (1 for none)
+ *   d_positions_or_null  int64[n_tokens] angles' positions; NULL: the
+ *                   token's place in the cache
+ *   d_hists_or_null uint32[n_hists][256], 4-byte aligned: adds the exponent
+ *                   counts (bits 14..7) of the keys and values written, as
+ *                   sz_histogram_accumulate would from the pages.  Request
+ *                   r's keys go to row d_hist_rows[r], its values to row
+ *                   d_hist_rows[n_reqs + r]; without d_hist_rows to rows r
+ *                   and n_reqs + r.  A row at or above n_hists gives
+ *                   SZ_ERR_INVALID.
+ * A request with more new tokens than kv_len gives SZ_ERR_INVALID.  The pages
+ * written must belong to one request each.  Norm, angle and rotation are
+ * computed in 32 bits (the angle's product and its reduction in 64) and
+ * rounded once.
+ */
+typedef struct sz_append_args {
+    const void *d_k;
+    const void *d_v;
+    uint64_t k_stride[2]; /* elements between tokens, heads */
+    uint64_t v_stride[2];
+    const void *d_q_or_null;
+    void *d_q_out;
+    uint64_t q_stride[2];
+    uint64_t q_out_stride[2];
+    const void *d_q_norm_or_null;
+    const void *d_k_norm_or_null;
+    const double *d_freqs_or_null;
+    const int64_t *d_positions_or_null;
+    uint32_t *d_hists_or_null;
+    const uint32_t *d_hist_rows_or_null;
+    uint32_t q_heads;
+    uint32_t rot_dim;
+    uint32_t interleaved;
+    uint32_t n_hists;
+    float rot_scale;
+    float eps;
+} sz_append_args;
+sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *args, int32_t *d_status, void *stream);
+
+/*
+ * sz_plan_attention -- workspace bytes of sz_paged_attention for any batch
+ * of this head_dim.  Host only.
+ *
+ * sz_paged_attention -- softmax attention of the new tokens' queries over
+ * the paged cache.  Query i of request r at position p = kv_len - n + i sees
+ * keys j < kv_len with j <= p if causal and, if window > 0, j > p - window.
+ *   s_j = scale * <q, k_j>;  out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+ *   d_q, d_out      rows of q_heads heads (a multiple of the KV heads: query
+ *                   head h reads KV head h / (q_heads / heads)); strides and
+ *                   alignment as in sz_append_args.  d_out may be d_q with
+ *                   the same strides.
+ *   d_lse_or_null   optional out float[n_tokens][q_heads]: m + log(sum), for
+ *                   joining results over parts of the keys
+ *   causal, window  window > 0 needs causal
+ *   d_ws, ws_bytes  workspace of sz_plan_attention's size, 16-byte aligned;
+ *                   calls that may overlap need one each
+ * A query that sees no key (kv_len 0, or more new tokens than kv_len) gets
+ * zeros and lse = -inf.  Cache contents at and behind kv_len are never used,
+ * whatever bits they hold.  Scores, sums and the running maximum are 32-bit;
+ * the weights exp(s - m) are rounded to the 16-bit type before they meet the
+ * values.  The result does not depend on timing: parts of a split row are
+ * joined in a fixed order.
+ */
+typedef struct sz_attention_args {
+    const void *d_q;
+    void *d_out;
+    uint64_t q_stride[2]; /* elements between tokens, heads */
+    uint64_t out_stride[2];
+    float *d_lse_or_null;
+    uint32_t q_heads;
+    uint32_t causal;
+    uint32_t window;
+    float scale;
+} sz_attention_args;
+sz_status sz_plan_attention(uint32_t head_dim, uint64_t *workspace_bytes);
+sz_status sz_paged_attention(const sz_paged_kv *kv, const sz_attention_args *args, int32_t *d_status, void *d_ws,
+                             uint64_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------- no-allocation path */
 /*
  * sz_encode_static -- the whole compression of one tensor (histogram,

@@ -30,6 +30,8 @@ __all__ = [
     "sz_select_codebook", "sz_select_codebook_batched", "select_codebooks", "sz_set_wait_limit_ns", "sz_debug_set_flags", "sz_tile_elems",
     "sz_version", "encode", "compress", "encode_one_pass", "decode", "BatchPlan", "lib",
     "HEADER_BYTES", "max_bytes", "STATUS",
+    "sz_paged_kv", "sz_append_args", "sz_attention_args", "sz_append_kv", "sz_plan_attention", "sz_paged_attention",
+    "append_kv", "paged_attention", "rope_frequencies",
 ]
 
 HEADER_BYTES = 48
@@ -51,6 +53,27 @@ class SzError(RuntimeError):
 class sz_segment(ctypes.Structure):
     _fields_ = [("n_elems", ctypes.c_uint64), ("page_begin", ctypes.c_uint64),
                 ("out_offset", ctypes.c_uint64), ("tile_begin", ctypes.c_uint64)]
+
+
+_U64, _U32, _VP, _F32 = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_float
+
+
+class sz_paged_kv(ctypes.Structure):
+    _fields_ = [("d_k", _VP), ("d_v", _VP), ("k_stride", _U64 * 3), ("v_stride", _U64 * 3), ("n_pages", _U64), ("heads", _U32),
+                ("head_dim", _U32), ("page_tokens", _U32), ("dtype", _U32), ("d_page_table", _VP), ("table_stride", _U64),
+                ("d_q_begin", _VP), ("d_kv_len", _VP), ("n_reqs", _U32), ("max_pages", _U32), ("n_tokens", _U64)]
+
+
+class sz_append_args(ctypes.Structure):
+    _fields_ = [("d_k", _VP), ("d_v", _VP), ("k_stride", _U64 * 2), ("v_stride", _U64 * 2), ("d_q_or_null", _VP), ("d_q_out", _VP),
+                ("q_stride", _U64 * 2), ("q_out_stride", _U64 * 2), ("d_q_norm_or_null", _VP), ("d_k_norm_or_null", _VP),
+                ("d_freqs_or_null", _VP), ("d_positions_or_null", _VP), ("d_hists_or_null", _VP), ("d_hist_rows_or_null", _VP),
+                ("q_heads", _U32), ("rot_dim", _U32), ("interleaved", _U32), ("n_hists", _U32), ("rot_scale", _F32), ("eps", _F32)]
+
+
+class sz_attention_args(ctypes.Structure):
+    _fields_ = [("d_q", _VP), ("d_out", _VP), ("q_stride", _U64 * 2), ("out_stride", _U64 * 2), ("d_lse_or_null", _VP),
+                ("q_heads", _U32), ("causal", _U32), ("window", _U32), ("scale", _F32)]
 
 
 _lib = None
@@ -84,6 +107,9 @@ def lib():
             "sz_histogram_accumulate_batched": [u32, vp, u64, vp, u64, vp, vp, vp, vp],
             "sz_select_codebook": [vp, vp, vp, vp],
             "sz_select_codebook_batched": [u32, vp, vp, vp, vp],
+            "sz_append_kv": [vp, vp, vp, vp],
+            "sz_plan_attention": [u32, pu64],
+            "sz_paged_attention": [vp, vp, vp, vp, u64, vp],
             "sz_set_wait_limit_ns": [u64],
             "sz_debug_set_flags": [u32],
         }
@@ -243,6 +269,22 @@ def sz_select_codebook(d_hist256, d_codebook16, d_escapes=None, stream=None):
 def sz_select_codebook_batched(n_hists, d_hists, d_codebooks, d_escapes=None, stream=None):
     _check(lib().sz_select_codebook_batched(n_hists, _p(d_hists), _p(d_codebooks), _p(d_escapes), _s(stream)),
            "sz_select_codebook_batched")
+
+
+def sz_append_kv(kv: sz_paged_kv, args: sz_append_args, d_status, stream=None):
+    _check(lib().sz_append_kv(ctypes.byref(kv), ctypes.byref(args), _p(d_status), _s(stream)), "sz_append_kv")
+
+
+def sz_plan_attention(head_dim: int) -> int:
+    """-> workspace bytes of sz_paged_attention"""
+    w = ctypes.c_uint64()
+    _check(lib().sz_plan_attention(head_dim, ctypes.byref(w)), "sz_plan_attention")
+    return w.value
+
+
+def sz_paged_attention(kv: sz_paged_kv, args: sz_attention_args, d_status, d_ws, ws_bytes, stream=None):
+    _check(lib().sz_paged_attention(ctypes.byref(kv), ctypes.byref(args), _p(d_status), _p(d_ws), ws_bytes, _s(stream)),
+           "sz_paged_attention")
 
 
 def sz_set_wait_limit_ns(limit_ns: int):
@@ -464,3 +506,6 @@ class BatchPlan:
     def container_bytes(self, k: int, size: int) -> "np.ndarray":
         off = int(self.out_offset[k])
         return self.container[off: off + size].cpu().numpy()
+
+
+from .paged import append_kv, paged_attention, rope_frequencies  # noqa: E402

@@ -1,0 +1,500 @@
+"""The paged-cache operators on the GPU against their 64-bit definitions
+(tests/paged_reference.py gives the values and the error bounds)."""
+import math
+import random
+
+import numpy as np
+import pytest
+
+import paged_reference as ref
+
+torch = pytest.importorskip("torch")
+import lossless_bf16_kv_splitzip_b200 as sz  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+DEV = "cuda:0"
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+class Batch:
+    """Random requests over scattered pages of a host copy of the cache; what
+    lies behind a request's end, in pages nobody owns and behind the last row
+    is NaN."""
+
+    def __init__(self, new, kv, heads, kv_heads, dim, page, dtype, seed=0, extra_rows=0, extra_pages=2, width=None):
+        g = torch.Generator().manual_seed(1000 + seed)
+        self.new, self.kv, self.heads, self.page, self.dtype = list(new), list(kv), heads, page, dtype
+        need = [-(-max(n, 0) // page) for n in kv]
+        total = sum(need) + extra_pages
+        self.k = torch.full((total, kv_heads, page, dim), math.nan, dtype=dtype)
+        self.v = self.k.clone()
+        order = list(range(total))
+        random.Random(seed).shuffle(order)
+        width = max(need + [1]) if width is None else width
+        self.table = torch.full((len(kv), width), -1, dtype=torch.int32)
+        for r, m in enumerate(need):
+            for i in range(m):
+                p = order.pop()
+                self.table[r, i] = p
+                t = min(page, kv[r] - i * page)
+                self.k[p, :, :t] = torch.randn((kv_heads, t, dim), generator=g).to(dtype)
+                self.v[p, :, :t] = torch.randn((kv_heads, t, dim), generator=g).to(dtype)
+        self.q_begin = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32)
+        self.kv_len = torch.tensor(list(kv), dtype=torch.int32)
+        self.rows = int(self.q_begin[-1]) + extra_rows
+        self.q = (1.5 * torch.randn((self.rows, heads, dim), generator=g)).to(dtype)
+        self.g = g
+
+    def cache(self):
+        return [t.to(DEV) for t in (self.k, self.v, self.table, self.q_begin, self.kv_len)]
+
+
+def check(got, want, tol, what=""):
+    got = got.cpu().double()
+    use = ~torch.isnan(tol)
+    assert bool(torch.isfinite(got[use]).all() | ~torch.isfinite(want[use]).all()), what + ": not finite"
+    same = got == want  # infinities
+    over = ((got - want).abs() - tol)[use & ~same]
+    assert over.numel() == 0 or float(over.max()) <= 0, "%s: %g over its bound, %d of %d values" % (
+        what, float(over.max()), int((over > 0).sum()), over.numel())
+
+
+def attend_and_check(b, causal=True, window=0, scale=None, **kw):
+    k, v, table, q_begin, kv_len = b.cache()
+    q = b.q.to(DEV)
+    out, lse, status = sz.paged_attention(q, k, v, table, q_begin, kv_len, scale=scale, causal=causal, window=window, return_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert status.cpu().tolist() == [0] * len(b.kv)
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, scale or 1 / math.sqrt(b.q.shape[2]), causal, window)
+    check(out, want[0], want[2], "out")
+    check(lse, want[1], want[3], "lse")
+    return out, lse
+
+
+SHAPES = [  # new tokens, cached tokens, query heads, KV heads, dim, page, type
+    ([1], [1], 4, 4, 64, 16, BF16),
+    ([1], [17], 32, 8, 128, 16, BF16),
+    ([1, 1, 1], [5, 300, 128], 8, 1, 128, 16, FP16),
+    ([1, 0, 3, 1], [40, 33, 3, 0], 8, 2, 64, 32, BF16),  # no new token; only new tokens; nothing cached
+    ([5, 5], [130, 515], 64, 8, 128, 16, FP16),
+    ([7], [7], 7, 1, 64, 8, BF16),  # a group of seven
+    ([129], [129], 2, 2, 128, 16, BF16),
+    ([257, 1, 64], [400, 257, 64], 4, 2, 128, 64, FP16),
+    ([300], [555], 12, 4, 64, 128, BF16),
+    ([33, 31], [129, 128], 28, 4, 128, 256, BF16),
+    ([40], [1000], 16, 1, 128, 24, FP16),  # pages that do not divide a tile
+    ([3, 9], [77, 9], 6, 2, 80, 16, BF16),
+    ([2, 30], [50, 31], 4, 1, 256, 16, FP16),
+    ([4], [21], 2, 1, 8, 5, BF16),
+    ([6, 1], [13, 29], 4, 2, 128, 1, FP16),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s[:6])).replace(" ", ""))
+@pytest.mark.parametrize("mode", ["causal", "full", "window"])
+def test_attention(shape, mode):
+    new, kv, hq, hk, dim, page, dtype = shape
+    attend_and_check(Batch(new, kv, hq, hk, dim, page, dtype), causal=mode != "full", window=37 if mode == "window" else 0)
+
+
+@pytest.mark.parametrize("window", [1, 16, 127, 128, 129, 1000])
+def test_attention_windows(window):
+    attend_and_check(Batch([200, 1, 3], [333, 401, 500], 8, 2, 64, 16, BF16, seed=window), window=window)
+
+
+@pytest.mark.parametrize("hq,hk,dim,dtype", [(4, 1, 128, BF16), (16, 4, 64, FP16), (2, 2, 128, FP16)])
+def test_attention_of_long_rows(hq, hk, dim, dtype):
+    # few rows over many keys: the keys are split over the whole GPU
+    attend_and_check(Batch([1, 2], [9001, 2300], hq, hk, dim, 16, dtype, seed=3))
+
+
+def test_attention_of_a_long_chunk():
+    attend_and_check(Batch([700, 90], [1500, 1203], 4, 1, 128, 16, BF16, seed=4))
+
+
+@pytest.mark.parametrize("dim,page", [(128, 16), (64, 64), (80, 16)])
+def test_more_new_tokens_than_cached(dim, page):
+    # the first rows stand before the cache's beginning and see nothing
+    out, lse = attend_and_check(Batch([9, 150, 4], [4, 20, 0], 4, 2, dim, page, BF16))
+    assert not out[:5].any() and bool((lse[:5] == -math.inf).all())
+
+
+@pytest.mark.parametrize("dim", [64, 128, 72])
+def test_extreme_scores(dim):
+    # scores of hundreds, equal scores, and the type's lowest value as a key
+    b = Batch([3, 130], [200, 131], 4, 2, dim, 16, BF16)
+    b.q *= 30
+    b.k[int(b.table[0, 1]), 0] = 0.0
+    b.k[int(b.table[0, 2]), 1, 3] = 100.0
+    attend_and_check(b, scale=0.5)
+    # keys hidden from a row may score anything: the last ones are visible to the last rows only
+    b = Batch([2], [130], 4, 2, dim, 16, BF16, seed=1)
+    b.q = b.q.abs()
+    page, at = int(b.table[0, 129 // 16]), 129 % 16
+    b.k[page, :, at] = torch.finfo(BF16).min
+    b.v[page, :, at] = 1.0
+    k, v, table, q_begin, kv_len = b.cache()
+    out, lse, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, return_lse=True)
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    assert bool(torch.isfinite(out).all())
+    check(out[:1], want[0][:1], want[2][:1])
+    # the last row scores -inf or the lowest number there: weight 0 either way
+    hidden = ref.attention(b.q[1:], b.k, b.v, b.table, torch.tensor([0, 1]), torch.tensor([129]), 1 / math.sqrt(dim))
+    check(out[1:], hidden[0], hidden[2])
+
+
+@pytest.mark.parametrize("dim", [128, 72])
+def test_infinite_and_nan_scores(dim):
+    b = Batch([1, 1, 1, 1], [20, 200, 20, 20], 2, 1, dim, 16, BF16)
+    b.q[:] = b.q.abs() + 0.1
+    b.k[int(b.table[0, 0]), :, 3] = -math.inf  # one key at -inf: weight 0
+    b.k[b.table[1].long()[: 200 // 16 + 1]] = -math.inf  # all at -inf: 0 / 0
+    b.k[int(b.table[2, 0]), :, 3] = math.nan
+    b.v[int(b.table[3, 1]), :, 2, 1] = math.inf
+    k, v, table, q_begin, kv_len = b.cache()
+    out, lse, _ = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, return_lse=True)
+    out, lse = out.float().cpu(), lse.cpu()
+    b.k[int(b.table[0, 0]), :, 3] = 0.0
+    keep = [j for j in range(20) if j != 3]
+    x = b.q[0].double()
+    K, V = ref.gather(b.k, b.table[0], 20)[keep, 0], ref.gather(b.v, b.table[0], 20)[keep, 0]
+    want = torch.softmax(x @ K.T / math.sqrt(dim), 1) @ V
+    assert float((out[0].double() - want).abs().max()) <= 2.0 ** -6 * float(V.abs().max())  # four half steps of the largest value
+    assert bool(out[1:3].isnan().all()) and bool((lse[1] == -math.inf).all()) and bool(lse[2].isnan().all())
+    assert bool(torch.isinf(out[3, :, 1]).all()) and bool(torch.isfinite(out[3, :, 2:]).all())
+
+
+@pytest.mark.parametrize("layout", ["token_major", "one_pool", "rows_of_a_projection", "in_place"])
+@pytest.mark.parametrize("dim", [128, 40])
+def test_attention_layouts(layout, dim):
+    b = Batch([5, 130, 1], [50, 131, 90], 8, 2, dim, 16, BF16, extra_rows=3)
+    k, v, table, q_begin, kv_len = b.cache()
+    q, out = b.q.to(DEV), None
+    if layout == "token_major":
+        k, v = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (k, v))
+    elif layout == "one_pool":
+        pool = torch.stack((k, v), 1)
+        k, v = pool[:, 0], pool[:, 1]
+        table = torch.cat((table, table), 1)[:, : table.shape[1]]
+    elif layout == "rows_of_a_projection":
+        row = torch.cat((q, torch.full((q.shape[0], 4, dim), math.nan, dtype=BF16, device=DEV)), 1)
+        q = row[:, :8]
+        out = torch.full((8, b.rows, dim), 7.0, dtype=BF16, device=DEV).transpose(0, 1)
+    else:
+        out = q
+    got, _, status = sz.paged_attention(q, k, v, table, q_begin, kv_len, out=out)
+    assert status.cpu().tolist() == [0, 0, 0]
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    check(got[: b.rows - 3], want[0][: b.rows - 3], want[2][: b.rows - 3])
+    if layout == "rows_of_a_projection":
+        assert bool((got[b.rows - 3:] == 7.0).all())  # rows of no request
+    if layout == "in_place":
+        assert torch.equal(got[b.rows - 3:].cpu(), b.q[b.rows - 3:])
+
+
+@pytest.mark.parametrize("dim", [128, 24])
+def test_pages_behind_the_window_may_be_gone(dim):
+    b = Batch([1, 20], [300, 200], 4, 2, dim, 16, BF16)
+    b.table[0, : (300 - 64) // 16] = -1
+    b.table[1, : (200 - 20 + 1 - 64) // 16] = 1 << 20
+    attend_and_check(b, window=64)
+
+
+@pytest.mark.parametrize("dim", [128, 24])
+def test_refused_requests(dim):
+    b = Batch([2, 1, 1, 1, 1], [40, 40, 20, 33, 9], 4, 2, dim, 16, BF16)
+    b.table[1, 1] = 1 << 30  # outside the pool
+    b.table[2, 0] = -5
+    b.kv_len[3] = 49  # the table holds 48
+    k, v, table, q_begin, kv_len = b.cache()
+    out, _, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len)
+    assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID, sz.SZ_ERR_CAPACITY, 0]
+    want = ref.attention(b.q[:2], b.k, b.v, b.table, torch.tensor([0, 2]), torch.tensor([40]), 1 / math.sqrt(dim))
+    check(out[:2], want[0], want[2])
+    new = torch.randn(6, 2, dim, dtype=torch.float32).to(BF16).to(DEV)
+    before = k.clone()
+    _, status = sz.append_kv(new, new, k, v, table, q_begin, torch.tensor([40, 17, 1, 49, 0], dtype=torch.int32, device=DEV))
+    # request 1's token would go to its bad page, request 4 has more tokens than its length
+    assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID, sz.SZ_ERR_CAPACITY, sz.SZ_ERR_INVALID]
+    changed = (k.view(torch.int16) != before.view(torch.int16)).any(-1).any(1).nonzero().cpu().tolist()
+    page = int(b.table[0, 2])
+    assert changed == [[page, 6], [page, 7]]
+    # rows out of order, or more than there are
+    bad = torch.tensor([0, 2, 1, 3, 9, 9], dtype=torch.int32, device=DEV)
+    table[:] = torch.arange(5, dtype=torch.int32, device=DEV)[:, None]
+    for call in (lambda: sz.paged_attention(b.q.to(DEV), k, v, table, bad, kv_len.clamp(max=16))[2],
+                 lambda: sz.append_kv(new, new, k, v, table, bad, kv_len.clamp(max=16))[1]):
+        assert call().cpu().tolist() == [0, sz.SZ_ERR_INVALID, 0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID]
+
+
+def test_attention_repeats_bit_for_bit_and_on_two_streams():
+    b = Batch([1, 3, 200], [5000, 700, 900], 8, 2, 128, 16, BF16)
+    args = [b.q.to(DEV)] + b.cache()
+    first, _, _ = sz.paged_attention(*args)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [sz.paged_attention(*args, stream=streams[i % 2])[0] for i in range(8)]
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, first)
+
+
+def test_captured_calls_follow_their_lengths():
+    b = Batch([1, 1, 2], [600, 40, 90], 8, 2, 128, 16, FP16, width=64)
+    k, v, table, q_begin, kv_len = b.cache()
+    q, out = b.q.to(DEV), torch.zeros_like(b.q, device=DEV)
+    new = torch.randn(4, 2, 128).to(FP16).to(DEV)
+    freqs = sz.rope_frequencies(128, device=DEV)
+    ws = torch.empty(sz.sz_plan_attention(128), dtype=torch.uint8, device=DEV)
+    q_rot = torch.empty_like(q)
+
+    def step():
+        sz.append_kv(new, new, k, v, table, q_begin, kv_len, q=q, q_out=q_rot, rope_freqs=freqs)
+        return sz.paged_attention(q_rot, k, v, table, q_begin, kv_len, out=out, workspace=ws)[2]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        status = step()
+    for kv in ([600, 40, 90], [3, 40, 2], [601, 33, 64]):
+        kv_len.copy_(torch.tensor(kv, dtype=torch.int32))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert status.cpu().tolist() == [0, 0, 0]
+        replayed = out.clone()
+        out.zero_()
+        step()
+        assert torch.equal(replayed, out)
+        want = ref.attention(q_rot.cpu(), k.cpu(), v.cpu(), b.table, b.q_begin, kv_len.cpu(), 1 / math.sqrt(128))
+        check(replayed, want[0], want[2])
+
+
+def test_two_captured_calls_share_a_workspace():
+    b = Batch([1, 2], [3000, 700], 8, 2, 128, 16, BF16)
+    c = Batch([200], [900], 8, 2, 128, 16, BF16, seed=9)
+    ws = torch.empty(sz.sz_plan_attention(128), dtype=torch.uint8, device=DEV)
+    calls, graphs = [], []
+    for x in (b, c):
+        args = [x.q.to(DEV)] + x.cache()
+        eager = sz.paged_attention(*args)[0].clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = sz.paged_attention(*args, workspace=ws)[0]
+        calls.append((out, eager, args))
+        graphs.append(g)
+    for _ in range(3):
+        for g, (out, eager, _) in zip(graphs, calls):
+            out.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for out, eager, _ in calls:
+            assert torch.equal(out, eager)
+
+
+def test_cache_beyond_32_bits():
+    # pools of more than 2^32 values; the request's pages lie at the end
+    P, H, D = 16, 8, 128
+    pages = (1 << 32) // (P * H * D) + 300
+    k = torch.empty((pages, H, P, D), dtype=BF16, device=DEV)
+    v = torch.empty_like(k)
+    b = Batch([3, 1], [40, 200], 16, 8, D, P, BF16)
+    k[-b.k.shape[0]:], v[-b.k.shape[0]:] = b.k.to(DEV), b.v.to(DEV)
+    _, _, table, q_begin, kv_len = b.cache()
+    far = torch.where(table >= 0, table + (pages - b.k.shape[0]), table).int()
+    out, _, status = sz.paged_attention(b.q.to(DEV), k, v, far, q_begin, kv_len)
+    assert status.cpu().tolist() == [0, 0]
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(D))
+    check(out, want[0], want[2])
+    new = torch.randn(4, H, D).to(BF16).to(DEV)
+    _, status = sz.append_kv(new, new, k, v, far, q_begin, kv_len)
+    assert status.cpu().tolist() == [0, 0]
+    for t, (r, at) in enumerate([(0, 37), (0, 38), (0, 39), (1, 199)]):
+        assert torch.equal(k[int(far[r, at // P]), :, at % P], new[t])
+        assert torch.equal(v[int(far[r, at // P]), :, at % P], new[t])
+
+
+# ------------------------------------------------------------------ append
+def append_and_check(b, rot=0, interleaved=False, norm=False, with_q=True, positions=None, scale=1.0, rows=None):
+    hk, dim = b.k.shape[1], b.k.shape[3]
+    tokens = b.rows
+    new_k, new_v = torch.randn((tokens, hk, dim), generator=b.g).to(b.dtype), torch.randn((tokens, hk, dim), generator=b.g).to(b.dtype)
+    freqs = sz.rope_frequencies(rot, 1e6) if rot else None
+    qw = (1 + 0.3 * torch.randn(dim, generator=b.g)).to(b.dtype) if norm and with_q else None
+    kw = (1 + 0.3 * torch.randn(dim, generator=b.g)).to(b.dtype) if norm else None
+    k, v, table, q_begin, kv_len = b.cache()
+    n = len(b.kv)
+    hists = torch.full((3 * n, 256), 5, dtype=torch.int32, device=DEV)
+
+    def dev(t):
+        return None if t is None else t.to(DEV)
+
+    q_out, status = sz.append_kv(new_k.to(DEV), new_v.to(DEV), k, v, table, q_begin, kv_len, q=b.q.to(DEV) if with_q else None,
+                                 rope_freqs=dev(freqs), rope_interleaved=interleaved, rope_scale=scale, positions=dev(positions),
+                                 q_norm=dev(qw), k_norm=dev(kw), eps=1e-5, hists=hists, hist_rows=dev(rows))
+    torch.cuda.synchronize()
+    assert status.cpu().tolist() == [0] * n
+    place = torch.zeros(tokens, dtype=torch.int64)
+    owner = [-1] * tokens
+    for r in range(n):
+        for i in range(b.new[r]):
+            t = int(b.q_begin[r]) + i
+            place[t], owner[t] = b.kv[r] - b.new[r] + i, r
+    pos = positions if positions is not None else place
+    want_k, tol_k = ref.turned(new_k, kw, 1e-5, freqs, pos, interleaved, scale)
+    got_k, got_v = k.cpu(), v.cpu()
+    counts = torch.full((3 * n, 256), 5, dtype=torch.int64)
+    at = rows.tolist() if rows is not None else list(range(2 * n))
+    touched = torch.zeros(b.k.shape[:3], dtype=torch.bool)
+    for t in range(tokens):
+        r = owner[t]
+        if r < 0:
+            continue
+        p, s = int(b.table[r, int(place[t]) // b.page]), int(place[t]) % b.page
+        touched[p, :, s] = True
+        check(got_k[p, :, s], want_k[t], tol_k[t], "k")
+        assert torch.equal(got_v[p, :, s], new_v[t])
+        for row, x in ((at[r], got_k[p, :, s]), (at[n + r], new_v[t])):
+            e = (x.contiguous().view(torch.int16).long() >> 7) & 255
+            counts[row] += torch.bincount(e.reshape(-1), minlength=256)
+    for got, was in ((got_k, b.k), (got_v, b.v)):  # nothing else changed, NaN patterns included
+        assert torch.equal(got.view(torch.int16)[~touched], was.view(torch.int16)[~touched])
+    assert torch.equal(hists.cpu().long(), counts)
+    if with_q:
+        want_q, tol_q = ref.turned(b.q, qw, 1e-5, freqs, pos, interleaved, scale)
+        mine = torch.tensor([o >= 0 for o in owner])
+        check(q_out.cpu()[mine], want_q[mine], tol_q[mine], "q")
+
+
+APPENDS = [  # new, cached, query heads, KV heads, dim, page, type
+    ([1], [1], 32, 8, 128, 16, BF16),
+    ([1, 1, 0, 1], [16, 17, 5, 300], 8, 2, 64, 16, FP16),
+    ([40, 3, 17], [40, 500, 33], 6, 3, 128, 32, BF16),
+    ([5, 64], [5, 80], 4, 1, 256, 8, FP16),
+    ([9], [20], 3, 1, 80, 5, BF16),
+    ([3], [3], 1, 1, 16, 1, BF16),
+    ([200], [1000], 28, 4, 128, 16, BF16),
+]
+
+
+@pytest.mark.parametrize("shape", APPENDS, ids=lambda s: "-".join(map(str, s[:6])).replace(" ", ""))
+@pytest.mark.parametrize("mode", ["plain", "half", "adjacent", "norm", "norm_half_part", "norm_adjacent_part", "no_q"])
+def test_append(shape, mode):
+    new, kv, hq, hk, dim, page, dtype = shape
+    b = Batch(new, kv, hq, hk, dim, page, dtype, extra_rows=2)
+    part = max(16, dim // 32 * 16)
+    append_and_check(b, rot={"plain": 0, "norm": 0, "norm_half_part": part, "norm_adjacent_part": part}.get(mode, dim), norm="norm" in mode,
+                     interleaved="adjacent" in mode, with_q=mode != "no_q", scale=1.25 if "part" in mode else 1.0)
+
+
+def test_append_at_far_positions():
+    b = Batch([30, 2], [40, 5], 4, 2, 128, 16, BF16)
+    far = torch.tensor([(1 << 20) * (i + 1) + i for i in range(30)] + [-7, 0], dtype=torch.int64)
+    append_and_check(b, rot=128, positions=far)
+
+
+def test_append_into_chosen_histogram_rows():
+    b = Batch([30, 2, 5], [40, 5, 5], 4, 2, 128, 16, BF16)
+    append_and_check(b, rot=64, rows=torch.tensor([4, 4, 0, 8, 7, 4], dtype=torch.int32))  # several requests in one row
+    k, v, table, q_begin, kv_len = b.cache()
+    new = torch.zeros((b.rows, 2, 128), dtype=BF16, device=DEV)
+    hists = torch.zeros((4, 256), dtype=torch.int32, device=DEV)
+    rows = torch.tensor([0, 1, 4, 0, -1, 3], dtype=torch.int32, device=DEV)
+    _, status = sz.append_kv(new, new, k, v, table, q_begin, kv_len, hists=hists, hist_rows=rows)
+    assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID]
+    assert int(hists.sum()) == 2 * 30 * 2 * 128 and int(hists[0].sum()) == int(hists.sum())
+
+
+@pytest.mark.parametrize("layout", ["token_major", "rows_of_a_projection"])
+def test_append_layouts_and_in_place(layout):
+    b = Batch([5, 20], [50, 31], 4, 2, 128, 16, BF16)
+    k, v, table, q_begin, kv_len = b.cache()
+    row = torch.randn(25, 8, 128).to(BF16).to(DEV)
+    freqs = sz.rope_frequencies(128, device=DEV)
+    plain = [row[:, :4].clone(), row[:, 4:6].clone(), row[:, 6:].clone()]
+    q0, _ = sz.append_kv(plain[1], plain[2], k, v, table, q_begin, kv_len, q=plain[0], rope_freqs=freqs)
+    k2, v2 = (t.to(DEV) for t in (b.k, b.v))
+    if layout == "token_major":
+        k2, v2 = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (k2, v2))
+    q = row[:, :4]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sz.append_kv(row[:, 4:6], row[:, 6:], k2, v2, table, q_begin, kv_len, q=q, q_out=q, rope_freqs=freqs, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(q, q0)
+    assert torch.equal(k2.contiguous().view(torch.int16), k.view(torch.int16)) and torch.equal(v2.contiguous().view(torch.int16), v.view(torch.int16))
+
+
+# --------------------------------------------------------------- together
+def test_prefill_transfer_and_continue():
+    """A prefill in chunks writes the cache and counts it, the codec ships the
+    pages to another pool, and decoding continues there: the containers are
+    the two-pass call's, and attention over the rebuilt pages is bit for bit
+    attention over the originals."""
+    R, HQ, HK, D, P = 3, 8, 2, 128, 16
+    total = [160, 64, 336]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    pages = sum(total) // P + R + 5
+    perm = torch.randperm(pages, generator=g, device=DEV).int()
+    width = max(total) // P + 1
+    table = torch.full((R, width), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for r in range(R):
+        table[r, : total[r] // P + 1] = perm[at: at + total[r] // P + 1]
+        at += total[r] // P + 1
+    k, v = (torch.zeros((pages, HK, P, D), dtype=BF16, device=DEV) for _ in range(2))
+    hists = torch.zeros((2 * R, 256), dtype=torch.int32, device=DEV)
+    freqs = sz.rope_frequencies(D, 500000.0, device=DEV)
+    norm = torch.ones(D, dtype=BF16, device=DEV)
+    done = [0] * R
+    outs = []
+    for share in (0.4, 1.0):
+        new = [int(total[r] * share) - done[r] for r in range(R)]
+        done = [d + n for d, n in zip(done, new)]
+        q_begin = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device=DEV)
+        kv_len = torch.tensor(done, dtype=torch.int32, device=DEV)
+        row = torch.randn((sum(new), HQ + 2 * HK, D), generator=g, device=DEV).to(BF16)
+        q, st = sz.append_kv(row[:, HQ:HQ + HK], row[:, HQ + HK:], k, v, table, q_begin, kv_len, q=row[:, :HQ], rope_freqs=freqs,
+                             q_norm=norm, k_norm=norm, hists=hists)
+        out, _, st2 = sz.paged_attention(q, k, v, table, q_begin, kv_len)
+        assert not st.any() and not st2.any()
+        want = ref.attention(q.cpu(), k.cpu(), v.cpu(), table.cpu(), q_begin.cpu(), kv_len.cpu(), 1 / math.sqrt(D))
+        check(out, want[0], want[2])
+        outs.append(out)
+    # the codec: keys of every request, then values, each request's pages one stream
+    elems = HK * P * D
+    lens = [n * HK * D for n in total] * 2
+    src = torch.cat([(t.data_ptr() + 2 * elems * table[r, : total[r] // P].long()) for t in (k, v) for r in range(R)])
+    plan = sz.BatchPlan(lens, elems, device=DEV)
+    cbs, _ = sz.select_codebooks(hists)
+    plan.encode_one_pass(src, cbs)
+    twice = sz.BatchPlan(lens, elems, device=DEV)
+    twice.encode(src)
+    torch.cuda.synchronize()
+    assert not plan.enc_status.any() and not twice.enc_status.any()
+    assert torch.equal(plan.sizes, twice.sizes)
+    for i in range(2 * R):
+        n = int(plan.sizes[i])
+        assert np.array_equal(plan.container_bytes(i, n), twice.container_bytes(i, n))
+    # the other side: its own pool and pages
+    k2, v2 = (torch.full_like(k, math.nan) for _ in range(2))
+    table2 = torch.where(table >= 0, pages - 1 - table, table)
+    dst = torch.cat([(t.data_ptr() + 2 * elems * table2[r, : total[r] // P].long()) for t in (k2, v2) for r in range(R)])
+    plan.decode(dst)
+    assert not plan.dec_status.any()
+    q_begin = torch.arange(R + 1, dtype=torch.int32, device=DEV)
+    kv_len = torch.tensor([n + 1 for n in total], dtype=torch.int32, device=DEV)
+    row = torch.randn((R, HQ + 2 * HK, D), generator=g, device=DEV).to(BF16)
+    got = []
+    for kk, vv, tt in ((k, v, table), (k2, v2, table2)):
+        q, st = sz.append_kv(row[:, HQ:HQ + HK], row[:, HQ + HK:], kk, vv, tt, q_begin, kv_len, q=row[:, :HQ], rope_freqs=freqs,
+                             q_norm=norm, k_norm=norm)
+        out, _, st2 = sz.paged_attention(q, kk, vv, tt, q_begin, kv_len)
+        assert not st.any() and not st2.any()
+        got.append(out)
+    assert torch.equal(got[0], got[1])
