@@ -5,7 +5,10 @@
 // to m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') +
 // e^(s - m') v; two such triples over different keys join the same way.
 // Exponentials are taken base 2 of scores scaled by log2(e).
+#include <type_traits>
+
 #include "sz_paged.cuh"
+#include "sz_tensor.cuh"
 
 namespace sz {
 
@@ -121,8 +124,876 @@ static cudaError_t launch_any_t(const sz_paged_kv &kv, const sz_attention_args &
     return cudaGetLastError();
 }
 
-cudaError_t launch_attention(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, cudaStream_t s) {
-    return kv.dtype == SZ_BF16 ? launch_any_t<__nv_bfloat16>(kv, a, status, s) : launch_any_t<__half>(kv, a, status, s);
+
+// ------------------------------------------------------- tensor-core kernel
+// Rows of one KV head -- (token, query head) pairs, tokens outermost -- form
+// blocks of kM tiles of up to 128; keys come in tiles of up to 128 whole
+// pages.  One unit of work is one key tile of one block; the units of all
+// requests, heads and blocks in order are dealt in equal runs to the CTAs,
+// so a block's keys may be split over several of them (their parts are
+// joined afterwards, in order) and a CTA may serve several blocks.
+//
+// Warps: kM * 4 hold one row per thread (softmax); one issues the products;
+// one issues the copies.  Per row tile X and key tile: S_X = Q_X K^T into
+// tensor memory, the softmax threads replace S_X by P_X = exp2(c S - c m) in
+// 16 bits in the same columns, O_X += P_X V.  While one row tile's softmax
+// runs, the tensor cores work on the other's products (kM = 2) or on the
+// other CTA's of the SM (kM = 1).
+//
+// The accumulator is rescaled only when a row's maximum has risen by more
+// than 2^8 since the reference that its weights were taken against: until
+// then weights up to 2^8 are as exact, and O stays untouched in tensor
+// memory.
+constexpr uint32_t kTileRows = 128;
+constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
+constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
+constexpr float kRescaleAt = 8.0f;
+constexpr uint64_t kMinUnits = 1;                       // least share of a CTA
+constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
+
+template <int D, int kM>
+struct Shape {
+    static constexpr int kHalves = D / 64;
+    static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+    static constexpr int kSoftmaxThreads = kM * 128;
+    static constexpr int kThreads = kSoftmaxThreads + 64;
+    static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
+    static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
+    static constexpr uint32_t kSmem = 1024 + kM * kTileBytes + kSlots * kTileBytes;
+    static constexpr uint32_t kPartFloats = kM * kTileRows * (D + 2);  // a block's rows, then (m, l) per row
+};
+
+// A block whose keys continue in the CTAs after the one that began it.
+struct SplitRec {
+    uint32_t r, head, block;
+    uint32_t last;  // last CTA with a part; 0: none
+};
+
+struct TensorArgs {
+    sz_paged_kv kv;
+    sz_attention_args a;
+    float c;               // scale * log2(e), positive
+    uint32_t group;        // query heads per KV head
+    uint32_t tile_tokens;  // new tokens per row tile
+    uint32_t key_tile;     // keys per tile
+    uint32_t box_tokens;   // keys per copy
+    uint32_t copies;       // copies per key tile and 64 channels
+    uint32_t ctas;
+    SplitRec *rec;         // [ctas]
+    uint32_t *failed;      // [ctas]
+    float *parts;          // [ctas][2][kPartFloats]: the part that continues a block, the part that begins one
+    uint64_t wait_limit_ns;
+    uint32_t debug_flags;
+};
+
+// Visible keys of tokens [first, end) of a request: [*begin, *stop).
+__device__ __forceinline__ void key_range(const TensorArgs &p, const Request &q, int32_t first, int32_t end, int32_t *begin,
+                                          int32_t *stop) {
+    const int32_t p0 = q.kv - q.n + first, p1 = q.kv - q.n + end;  // position of the first, one past the last
+    *stop = p.a.causal ? max(0, min(q.kv, p1)) : q.kv;
+    *begin = p.a.window ? (int32_t)max((int64_t)0, (int64_t)p0 - p.a.window + 1) : 0;
+}
+
+// Key tiles [lo, hi) of block b; at least one, so that rows which see nothing
+// are written too.
+template <int kM>
+__device__ __forceinline__ void block_tiles(const TensorArgs &p, const Request &q, uint32_t b, int32_t *lo, int32_t *hi) {
+    const int32_t span = (int32_t)(kM * p.tile_tokens);
+    const int32_t first = (int32_t)b * span;
+    int32_t begin, stop;
+    key_range(p, q, first, min(q.n, first + span), &begin, &stop);
+    *lo = begin / (int32_t)p.key_tile;
+    *hi = max(*lo + 1, (stop + (int32_t)p.key_tile - 1) / (int32_t)p.key_tile);
+}
+
+template <int kM>
+__device__ __forceinline__ uint32_t block_count(const TensorArgs &p, const Request &q) {
+    const uint32_t span = kM * p.tile_tokens;
+    return ((uint32_t)q.n + span - 1) / span;
+}
+
+// Where a CTA stands in the order of units.
+struct Cursor {
+    uint32_t r, head, block, off;  // off: tiles of the block done by earlier CTAs
+    uint64_t left;                 // units still to do
+    Request q;
+};
+struct Piece {
+    uint32_t r, head, block;
+    int32_t t0, t1;     // key tiles
+    bool starts, ends;  // holds the block's first, last tile
+    Request q;
+};
+
+template <int kM>
+__device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece &w) {
+    if (c.left == 0) return false;
+    int32_t lo, hi;
+    block_tiles<kM>(p, c.q, c.block, &lo, &hi);
+    w.r = c.r;
+    w.head = c.head;
+    w.block = c.block;
+    w.q = c.q;
+    w.t0 = lo + (int32_t)c.off;
+    const uint32_t n = (uint32_t)umin64((uint64_t)(hi - w.t0), c.left);
+    w.t1 = w.t0 + (int32_t)n;
+    w.starts = c.off == 0;
+    w.ends = w.t1 == hi;
+    c.left -= n;
+    c.off = 0;
+    if (++c.block >= block_count<kM>(p, c.q)) {
+        c.block = 0;
+        if (++c.head >= p.kv.heads) {
+            c.head = 0;
+            while (c.left > 0 && ++c.r < p.kv.n_reqs) {
+                c.q = load_request(p.kv, c.r);
+                if (c.q.n > 0) break;
+            }
+            if (c.r >= p.kv.n_reqs) c.left = 0;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v, uint32_t lane) {  // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= (uint32_t)d) v += y;
+    }
+    return v;
+}
+
+// Units per KV head of request `r0 + lane` (0 past the end), by one warp:
+// requests of a few blocks are summed by their lane, larger ones by all.
+template <int kM>
+__device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane) {
+    Request q;
+    q.q0 = q.n = q.kv = 0;
+    q.status = SZ_OK;
+    if (r < p.kv.n_reqs) q = load_request(p.kv, r);
+    const uint32_t blocks = block_count<kM>(p, q);
+    uint64_t units = 0;
+    int32_t lo, hi;
+    if (blocks <= 4)
+        for (uint32_t b = 0; b < blocks; ++b) {
+            block_tiles<kM>(p, q, b, &lo, &hi);
+            units += (uint32_t)(hi - lo);
+        }
+    uint32_t many = __ballot_sync(0xFFFFFFFFu, blocks > 4);
+    while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        Request x;
+        x.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, src);
+        x.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+        x.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
+        const uint32_t n = block_count<kM>(p, x);
+        uint64_t sum = 0;
+        for (uint32_t b = lane; b < n; b += 32) {
+            block_tiles<kM>(p, x, b, &lo, &hi);
+            sum += (uint32_t)(hi - lo);
+        }
+        sum = warp_sum(sum);
+        if ((int)lane == src) units = sum;
+    }
+    return units;
+}
+
+struct PlanShared {
+    uint64_t warp_units[16];
+    uint64_t total;
+    uint64_t left;
+    uint32_t used;  // CTAs with work
+    uint32_t r, head, block, off;
+};
+
+// This CTA's share of the units, found by all of its threads.
+template <int kM, int kThreads>
+__device__ void find_share(const TensorArgs &p, PlanShared &s) {
+    constexpr uint32_t kW = kThreads / 32;
+    const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const uint32_t rounds = (uint32_t)div_up(div_up(p.kv.n_reqs, 32), kW);
+    uint64_t mine = 0;
+    for (uint32_t i = 0; i < rounds; ++i)
+        mine += lane_units<kM>(p, (wid * rounds + i) * 32 + lane, lane);
+    mine = warp_sum(mine) * p.kv.heads;
+    if (lane == 0) s.warp_units[wid] = mine;
+    __syncthreads();
+    uint64_t total = 0, before = 0;
+    for (uint32_t w = 0; w < kW; ++w) {
+        if (w < wid) before += s.warp_units[w];
+        total += s.warp_units[w];
+    }
+    // every CTA that works has at least one unit, so that the parts of a block
+    // are those of consecutive CTAs
+    const uint32_t used = (uint32_t)umin64(p.ctas, umax64(1, total / kMinUnits));
+    const bool works = blockIdx.x < used;
+    const uint64_t u0 = works ? blockIdx.x * total / used : 0, u1 = works ? (blockIdx.x + 1) * total / used : 0;
+    if (threadIdx.x == 0) {
+        s.left = 0;
+        s.total = total;
+        s.used = used;
+        s.r = s.head = s.block = s.off = 0;
+    }
+    __syncthreads();
+    if (u1 > u0 && u0 >= before && u0 < before + mine) {  // one warp
+        uint64_t rem = u0 - before;
+        for (uint32_t i = 0; i < rounds; ++i) {
+            const uint32_t r0 = (wid * rounds + i) * 32;
+            const uint64_t per_head = lane_units<kM>(p, r0 + lane, lane);
+            const uint64_t end = warp_scan(per_head * p.kv.heads, lane);
+            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rem < end);
+            if (hit == 0) {
+                rem -= __shfl_sync(0xFFFFFFFFu, end, 31);
+                continue;
+            }
+            const int src = __ffs(hit) - 1;
+            const uint64_t w = __shfl_sync(0xFFFFFFFFu, per_head, src);
+            rem -= __shfl_sync(0xFFFFFFFFu, end - per_head * p.kv.heads, src);
+            const uint32_t r = r0 + (uint32_t)src;
+            const uint32_t head = (uint32_t)(rem / w);
+            rem -= head * w;
+            const Request q = load_request(p.kv, r);
+            for (uint32_t b0 = 0; b0 < block_count<kM>(p, q); b0 += 32) {
+                uint64_t n = 0;
+                if (b0 + lane < block_count<kM>(p, q)) {
+                    int32_t lo, hi;
+                    block_tiles<kM>(p, q, b0 + lane, &lo, &hi);
+                    n = (uint32_t)(hi - lo);
+                }
+                const uint64_t stop = warp_scan(n, lane);
+                const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < stop);
+                if (here == 0) {
+                    rem -= __shfl_sync(0xFFFFFFFFu, stop, 31);
+                    continue;
+                }
+                const int at = __ffs(here) - 1;
+                rem -= __shfl_sync(0xFFFFFFFFu, stop - n, at);
+                if (lane == 0) {
+                    s.r = r;
+                    s.head = head;
+                    s.block = b0 + (uint32_t)at;
+                    s.off = (uint32_t)rem;
+                    s.left = u1 - u0;
+                }
+                break;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// Wait for a phase, by all lanes of a warp: false when the limit of device
+// time ran out here or elsewhere in the CTA.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            if (*failed) break;
+            if (globaltimer_ns() - t0 > limit_ns) {
+                *failed = 1u;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct Bars {
+    uint64_t full[10], empty[10];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t drain;
+};
+
+template <typename T, int D, int kM>
+__global__ void __launch_bounds__(Shape<D, kM>::kThreads, Shape<D, kM>::kCtasPerSm)
+attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using S = Shape<D, kM>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kScoreWord = mma_word(kBf16, 128, false);
+    constexpr uint32_t kOutWord = mma_word(kBf16, D, true);
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    __shared__ PlanShared plan;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ uint32_t failed;
+    const uint32_t tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t ring0 = smem0 + kM * S::kTileBytes;
+    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1;
+
+    if (wid == kMmaWarp) tmem_alloc(&tmem_base_s, S::kColumns);
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_empty, 1);
+        for (int x = 0; x < kM; ++x) {
+            mbar_init(&bars.s_full[x], 1);
+            mbar_init(&bars.p_full[x], 4);
+            mbar_init(&bars.pv_done[x], 1);
+        }
+        mbar_init(&bars.drain, 1);
+        fence_mbar_init();
+        failed = 0;
+    }
+    if (wid == kCopyWarp && lane == 0) {
+        prefetch_map(&q_map);
+        prefetch_map(&k_map);
+        prefetch_map(&v_map);
+    }
+    // Rows of a tile that no copy writes (pages that do not divide 128) hold
+    // zeros from here on: their weights are 0, and so must be what they meet.
+    if (p.key_tile < kTileRows)
+        for (uint32_t i = tid; i < S::kSlots * S::kHalves * (kTileRows - p.key_tile) * 8; i += S::kThreads) {
+            const uint32_t piece = i % 8, row = p.key_tile + i / 8 % (kTileRows - p.key_tile), half = i / 8 / (kTileRows - p.key_tile);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring0 + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0) : "memory");
+        }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    find_share<kM, S::kThreads>(p, plan);  // synchronises the block
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    allow_dependents();
+    const uint32_t tmem = tmem_base_s;
+    Cursor cur;
+    cur.r = plan.r;
+    cur.head = plan.head;
+    cur.block = plan.block;
+    cur.off = plan.off;
+    cur.left = plan.left;
+    if (cur.left > 0) cur.q = load_request(p.kv, cur.r);
+    volatile uint32_t *const fail = &failed;
+    const uint64_t limit = p.wait_limit_ns;
+    Piece w;
+
+    if (wid == kCopyWarp) {
+        // ------------------------------------------------------------ copies
+        const bool silent = (p.debug_flags & kDebugNoSignal) != 0;
+        const uint32_t my_copy = lane / S::kHalves, my_half = lane % S::kHalves;
+        const bool mine = my_copy < p.copies;
+        const uint32_t tile_bytes = p.key_tile * S::kHalves * kRowBytes;
+        const uint32_t dst_off = my_half * kHalfBytes + my_copy * p.box_tokens * kRowBytes;
+        uint32_t use = 0, pieces = 0;  // ring uses, pieces begun
+        bool ok = true;
+        SplitRec rec;
+        rec.r = rec.head = rec.block = rec.last = 0;
+        uint64_t unit = blockIdx.x * plan.total / plan.used;
+        while (ok && next_piece<kM>(p, cur, w)) {
+            if (w.starts && !w.ends) {  // goes on in the CTAs up to the one that holds its last unit
+                int32_t lo, hi;
+                block_tiles<kM>(p, w.q, w.block, &lo, &hi);
+                rec.r = w.r;
+                rec.head = w.head;
+                rec.block = w.block;
+                rec.last = (uint32_t)(((unit + (uint32_t)(hi - lo)) * plan.used - 1) / plan.total);
+            }
+            unit += (uint32_t)(w.t1 - w.t0);
+            const uint32_t first = w.block * kM * p.tile_tokens;
+            const uint32_t tokens = umin32((uint32_t)w.q.n - first, kM * p.tile_tokens);
+            const uint32_t tiles = kM == 1 || tokens <= p.tile_tokens ? 1u : 2u;
+            if (!(ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, fail, limit))) break;
+            ++pieces;
+            if (lane == 0) {
+                const uint32_t rows = p.tile_tokens * p.group;
+                mbar_arrive_expect_tx(&bars.q_full, tiles * rows * S::kHalves * kRowBytes);
+                if (!silent)
+                    for (uint32_t x = 0; x < tiles; ++x)
+                        for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
+                            tma_load_3d(smem0 + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(w.head * p.group),
+                                        (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full));
+            }
+            int32_t begin, stop;
+            key_range(p, w.q, (int32_t)first, (int32_t)(first + tokens), &begin, &stop);
+            const int32_t page_lo = begin / (int32_t)p.kv.page_tokens;
+            const int32_t page_hi = (w.q.kv + (int32_t)p.kv.page_tokens - 1) / (int32_t)p.kv.page_tokens;
+            // Pages behind the last token, before the window or outside the
+            // pool are copied from behind the pool's end: zeros.
+            auto page_at = [&](int32_t t) -> int32_t {
+                const int32_t i = t * (int32_t)p.key_tile / (int32_t)p.kv.page_tokens + (int32_t)my_copy;
+                int32_t page = -1;
+                if (mine && i >= page_lo && i < page_hi) page = page_of(p.kv, w.r, (uint32_t)i);
+                return page < 0 ? (int32_t)p.kv.n_pages : page;
+            };
+            int32_t page = page_at(w.t0);
+            for (int32_t t = w.t0; t < w.t1 && ok; ++t) {
+                const int32_t slot_tok = p.box_tokens < p.kv.page_tokens ? t * (int32_t)p.key_tile % (int32_t)p.kv.page_tokens : 0;
+                const int32_t next = t + 1 < w.t1 ? page_at(t + 1) : 0;
+                for (int kv2 = 0; kv2 < 2; ++kv2) {
+                    const uint32_t slot = use % S::kSlots, phase = use / S::kSlots & 1;
+                    if (!(ok = warp_wait(&bars.empty[slot], phase ^ 1, fail, limit))) break;
+                    ++use;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars.full[slot], tile_bytes);
+                    __syncwarp();
+                    if (mine && !silent)
+                        tma_load_4d(ring0 + slot * S::kTileBytes + dst_off, kv2 ? &v_map : &k_map, (int)(my_half * 64), slot_tok,
+                                    (int)w.head, page, smem_u32(&bars.full[slot]));
+                }
+                page = next;
+            }
+        }
+        if (lane == 0) p.rec[blockIdx.x] = rec;
+        if (!ok && !silent) {  // copies still under way must land before the CTA ends
+            const uint32_t from = use > (uint32_t)S::kSlots ? use - S::kSlots : 0;
+            for (uint32_t u = from; u < use; ++u) mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
+            if (pieces) mbar_wait(&bars.q_full, (pieces - 1) & 1, limit);
+        }
+    } else if (wid == kMmaWarp) {
+        // ---------------------------------------------------------- products
+        uint32_t done[2] = {0, 0};  // score products per row tile
+        uint32_t g = 0, pieces = 0;
+        auto active = [&](const Piece &x, int m) {
+            return (uint32_t)x.q.n - x.block * kM * p.tile_tokens > (uint32_t)m * p.tile_tokens;
+        };
+        auto slot_of = [&](uint32_t use) { return use % S::kSlots; };
+        auto score = [&](int m, uint32_t use) {  // S_m = Q_m K^T
+            if (lane == 0) {
+                const uint32_t qb = smem0 + m * S::kTileBytes, kb = ring0 + slot_of(use) * S::kTileBytes;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = (uint32_t)(i / 4) * kHalfBytes + (uint32_t)(i % 4) * 32;
+                    mma_smem(tmem + m * 128, operand_desc(qb + off, 16), operand_desc(kb + off, 16), kScoreWord, i > 0);
+                }
+                mma_commit(&bars.s_full[m]);
+            }
+            ++done[m];
+        };
+        bool ok = true;
+        bool have = next_piece<kM>(p, cur, w);
+        int32_t t = have ? w.t0 : 0;
+        if (have) {
+            ok = warp_wait(&bars.q_full, 0, fail, limit) && warp_wait(&bars.full[0], 0, fail, limit);
+            ++pieces;
+            if (ok) {
+                tc_fence_after();
+                for (int m = 0; m < kM; ++m)
+                    if (active(w, m)) score(m, 0);
+                if (lane == 0) {
+                    mma_commit(&bars.empty[0]);
+                    if (w.t0 + 1 == w.t1) mma_commit(&bars.q_empty);
+                }
+            }
+        }
+        while (have && ok) {
+            Piece nw = w;
+            int32_t nt = t + 1;
+            bool more = true;
+            if (nt >= w.t1) {
+                more = next_piece<kM>(p, cur, nw);
+                nt = nw.t0;
+            }
+            const uint32_t vu = 2 * g + 1, ku = 2 * g + 2;
+            bool v_ready = false, k_ready = false;
+            // keys behind the last token in this tile's last page: their
+            // weights are 0, so their values must be finite
+            const int32_t z0 = w.q.kv - t * (int32_t)p.key_tile;
+            for (int m = 0; m < kM && ok; ++m) {
+                if (active(w, m)) {
+                    if (!v_ready) {
+                        if (!(ok = warp_wait(&bars.full[slot_of(vu)], vu / S::kSlots & 1, fail, limit))) break;
+                        v_ready = true;
+                        if (z0 > 0 && z0 < (int32_t)p.key_tile) {
+                            const int32_t page = (int32_t)p.kv.page_tokens;
+                            const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)w.q.kv + page - 1) / page * page - (int64_t)t * p.key_tile);
+                            const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+                            for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
+                                const uint32_t piece = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0)
+                                             : "memory");
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                        }
+                    }
+                    if (!(ok = warp_wait(&bars.p_full[m], (done[m] - 1) & 1, fail, limit))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+#pragma unroll
+                        for (int i = 0; i < (int)kTileRows / 16; ++i)
+                            mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, operand_desc(vb + i * 16 * kRowBytes, kHalfBytes), kOutWord,
+                                     (t > w.t0 || i > 0) ? 1u : 0u);
+                        mma_commit(&bars.pv_done[m]);
+                    }
+                }
+                if (more && active(nw, m)) {
+                    if (!k_ready) {
+                        if (nt == nw.t0) {
+                            if (!(ok = warp_wait(&bars.q_full, pieces & 1, fail, limit))) break;
+                            ++pieces;
+                        }
+                        if (!(ok = warp_wait(&bars.full[slot_of(ku)], ku / S::kSlots & 1, fail, limit))) break;
+                        k_ready = true;
+                        tc_fence_after();
+                    }
+                    score(m, ku);
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                mma_commit(&bars.empty[slot_of(vu)]);
+                if (more) {
+                    mma_commit(&bars.empty[slot_of(ku)]);
+                    if (nt + 1 == nw.t1) mma_commit(&bars.q_empty);
+                }
+            }
+            __syncwarp();
+            w = nw;
+            t = nt;
+            have = more;
+            ++g;
+        }
+        if (!ok) {  // products under way must end before their memory is given back
+            if (lane == 0) {
+                mma_commit(&bars.drain);
+                mbar_wait(&bars.drain, 0, limit);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ----------------------------------------------------------- softmax
+        const uint32_t m_tile = wid / 4;
+        const uint32_t row = tid & 127;
+        const uint32_t lanes = (wid & 3) * 32;  // this warp's lanes of tensor memory
+        const uint32_t s_at = tmem + (lanes << 16) + m_tile * 128;
+        const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D;
+        const uint32_t my_token = row / p.group, my_head = row % p.group;
+        uint32_t n = 0;  // tiles done by this row tile
+        bool ok = true;
+        while (ok && next_piece<kM>(p, cur, w)) {
+            const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
+            if ((uint32_t)w.q.n <= first) continue;
+            const uint32_t rows = umin32((uint32_t)w.q.n - first, p.tile_tokens) * p.group;
+            const bool warp_live = lanes < rows;
+            int32_t begin, stop;
+            key_range(p, w.q, (int32_t)(first + my_token), (int32_t)(first + my_token) + 1, &begin, &stop);
+            float m = -INFINITY, l = 0.0f;  // reference of the weights, their sum
+            for (int32_t t = w.t0; t < w.t1; ++t, ++n) {
+                if (!(ok = warp_wait(&bars.s_full[m_tile], n & 1, fail, limit))) break;
+                tc_fence_after();
+                if (warp_live) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s[i]);
+                    tmem_wait_ld();
+                    const int32_t k0 = t * (int32_t)p.key_tile;
+                    const int32_t from = max(begin - k0, 0), to = min(stop - k0, (int32_t)p.key_tile);
+                    if (__any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const int32_t col = i * 32 + j;
+                                if (col < from || col >= to) s[i][j] = 0xFF800000u;  // -inf
+                            }
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(s[i][j]));
+                    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (t == w.t0) {
+                        m = high;
+                    } else {
+                        const bool rise = (high - m) * p.c > kRescaleAt;
+                        if (__any_sync(0xFFFFFFFFu, rise)) {
+                            // the accumulator as of the tile before
+                            if (!(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
+                            tc_fence_after();
+                            const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
+                            if (rise) m = high;
+                            l *= f;
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + i * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st32(o_at + i * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w16[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float a = exp2_fast(fmaf(__uint_as_float(s[i][2 * j]), p.c, -ref));
+                            const float b = exp2_fast(fmaf(__uint_as_float(s[i][2 * j + 1]), p.c, -ref));
+                            sum[i] += a;
+                            sum[(i + 1) & 3] += b;
+                            w16[j] = Half2<T>::narrow(a, b);
+                        }
+                        tmem_st16(s_at + i * 16, w16);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[m_tile]);
+            }
+            if (!ok || !(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
+            tc_fence_after();
+            if (!warp_live) continue;
+            const bool mine = row < rows;
+            const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
+            const float ref = m * p.c;  // log2 units
+            if (w.starts && w.ends) {
+                const bool any = begin < stop;
+                const float inv = any ? 1.0f / l : 0.0f;
+                uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + i * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = any ? __uint_as_float(o[8 * j + e]) * inv : 0.0f;
+                        if (mine) *(uint4 *)(out + i * 32 + j * 8) = narrow8<T>(x);
+                    }
+                }
+                if (mine && p.a.d_lse_or_null)
+                    p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any ? (l > 0.0f || l != l ? (ref + log2f(l)) * kLn2 : -INFINITY) : -INFINITY;
+            } else {
+                float *part = p.parts + (size_t)(blockIdx.x * 2 + (w.starts ? 1 : 0)) * S::kPartFloats;
+                const uint32_t at = m_tile * kTileRows + row;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + i * 32, o);
+                    tmem_wait_ld();
+                    if (mine)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *(uint4 *)(part + (size_t)at * D + i * 32 + j * 4) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+                if (mine) *(float2 *)(part + kM * kTileRows * D + at * 2) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
+            }
+        }
+        tc_fence_before();
+    }
+    // ------------------------------------------------------------------ end
+    __syncthreads();
+    if (tid == 0) p.failed[blockIdx.x] = failed;
+    if (wid == kMmaWarp) tmem_free(tmem, S::kColumns);
+}
+
+// Statuses of all requests, then the blocks whose keys were split: a warp per
+// row joins its parts in order.
+constexpr int kJoinThreads = 256;
+constexpr uint32_t kJoinY = 4;
+
+template <typename T, int D, int kM>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ TensorArgs p, int32_t *status) {
+    using S = Shape<D, kM>;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    // lengths and tables were there before the attention kernel began
+    const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, blocks = gridDim.x * gridDim.y;
+    for (uint32_t r = block; r < p.kv.n_reqs; r += blocks) {
+        const Request q = load_request(p.kv, r);
+        bool bad = false;
+        if (q.status == SZ_OK && q.n > 0 && q.kv > 0) {
+            int32_t begin, stop;
+            key_range(p, q, 0, q.n, &begin, &stop);
+            for (uint32_t i = (uint32_t)begin / p.kv.page_tokens + tid; i < (uint32_t)(q.kv - 1) / p.kv.page_tokens + 1; i += kJoinThreads)
+                bad |= page_of(p.kv, r, i) < 0;
+        }
+        bad = __syncthreads_or(bad) != 0;
+        if (tid == 0) status[r] = q.status != SZ_OK ? q.status : bad ? SZ_ERR_INVALID : SZ_OK;
+    }
+    grid_dependency_wait();
+    uint32_t late = 0;
+    for (uint32_t c = tid; c < p.ctas; c += kJoinThreads) late |= p.failed[c];
+    if (__syncthreads_or(late != 0)) {  // some rows were never finished
+        if (tid == 0)
+            for (uint32_t r = block; r < p.kv.n_reqs; r += blocks)
+                if (status[r] == SZ_OK) status[r] = SZ_ERR_DEVICE_TIMEOUT;
+        return;
+    }
+    const uint32_t c0 = blockIdx.x;
+    const SplitRec rec = p.rec[c0];
+    if (rec.last == 0) return;
+    const Request q = load_request(p.kv, rec.r);
+    const uint32_t first = rec.block * kM * p.tile_tokens;
+    const uint32_t tokens = umin32((uint32_t)q.n - first, kM * p.tile_tokens);
+    const uint32_t parts = rec.last - c0 + 1;
+    for (uint32_t i = blockIdx.y * (kJoinThreads / 32) + wid; i < tokens * p.group; i += kJoinY * (kJoinThreads / 32)) {
+        const uint32_t tok = i / p.group, g = i % p.group;
+        const uint32_t at = tok / p.tile_tokens * kTileRows + (tok % p.tile_tokens) * p.group + g;
+        auto part_of = [&](uint32_t k) { return p.parts + (size_t)(k == 0 ? c0 * 2 + 1 : (c0 + k) * 2) * S::kPartFloats; };
+        float top = -INFINITY;
+        for (uint32_t k = lane; k < parts; k += 32) top = fmaxf(top, part_of(k)[kM * kTileRows * D + at * 2]);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float sum = 0.0f, o[D / 32] = {};
+#pragma unroll 4
+        for (uint32_t k = 0; k < parts; ++k) {
+            const float *part = part_of(k);
+            const float2 ml = *(const float2 *)(part + kM * kTileRows * D + at * 2);
+            if (ml.y == 0.0f) continue;  // nothing visible there
+            const float f = exp2f(ml.x - top);
+            sum += ml.y * f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) o[e] += part[(size_t)at * D + lane * (D / 32) + e] * f;
+        }
+        int32_t begin, stop;
+        key_range(p, q, (int32_t)(first + tok), (int32_t)(first + tok) + 1, &begin, &stop);
+        const bool any = begin < stop;
+        const float inv = any ? 1.0f / sum : 0.0f;
+        const uint32_t token = (uint32_t)q.q0 + first + tok, head = rec.head * p.group + g;
+        uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+            *(uint32_t *)(out + lane * (D / 32) + 2 * e) =
+                any ? Half2<T>::narrow(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+        if (lane == 0 && p.a.d_lse_or_null)
+            p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any && sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------- host side
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(fn);
+    }();
+    return f;
+}
+
+// A map over `rank` dimensions, channels first.  A dimension of size 1 may
+// come with any stride; the map gets a legal one.
+static bool make_map(CUtensorMap *map, uint32_t dtype, void *base, int rank, const uint64_t *size, const uint64_t *stride_elems,
+                     const uint32_t *box) {
+    cuuint64_t dims[4], strides[3];
+    cuuint32_t boxes[4], steps[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = size[i];
+        boxes[i] = box[i];
+        if (i) strides[i - 1] = size[i] > 1 ? stride_elems[i] * 2 : size[0] * 2;
+    }
+    return encode_tiled()(map, dtype == SZ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                          base, dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Which shapes the tensor-core kernel takes: heads of 64 or 128 channels, a
+// positive scale (the running maximum is of unscaled scores), row tiles that
+// hold a whole group, and pages whose copies start on a swizzle group of 8
+// rows and fill or divide a tile.
+static bool tensor_shape(const sz_paged_kv &kv, const sz_attention_args &a) {
+    if (kv.head_dim != 64 && kv.head_dim != 128) return false;
+    if (!(a.scale > 0.0f) || !(a.scale < 1e30f)) return false;
+    if (a.q_heads / kv.heads > kTileRows || kv.n_pages == 0 || kv.n_tokens == 0) return false;
+    return kv.page_tokens % 8 == 0 && (kv.page_tokens <= kTileRows || kv.page_tokens % kTileRows == 0);
+}
+
+template <int D, int kM>
+static uint64_t tensor_workspace() {
+    const uint64_t ctas = (uint64_t)kMaxTensorSms * Shape<D, kM>::kCtasPerSm;
+    return ctas * (sizeof(SplitRec) + 16 + 2 * 4ull * Shape<D, kM>::kPartFloats);
+}
+
+uint64_t attention_workspace(uint32_t head_dim) {
+    if (head_dim == 128) return umax64(tensor_workspace<128, 1>(), tensor_workspace<128, 2>());
+    if (head_dim == 64) return umax64(tensor_workspace<64, 1>(), tensor_workspace<64, 2>());
+    return 256;
+}
+
+template <typename T, int D, int kM>
+static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, void *ws, const DeviceInfo &dev,
+                                 cudaStream_t s) {
+    using S = Shape<D, kM>;
+    TensorArgs p{};
+    p.kv = kv;
+    p.a = a;
+    p.c = a.scale * kLog2e;
+    if (!(p.c > 1e-37f)) p.c = 1e-37f;  // a hidden score is -inf, and -inf * 0 would be NaN
+    p.group = a.q_heads / kv.heads;
+    p.tile_tokens = kTileRows / p.group;
+    p.box_tokens = umin32(kv.page_tokens, kTileRows);
+    p.copies = kTileRows / p.box_tokens;
+    p.key_tile = p.copies * p.box_tokens;
+    p.ctas = umin32((uint32_t)dev.sms, kMaxTensorSms) * S::kCtasPerSm;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    p.parts = reinterpret_cast<float *>(at);
+    at += (size_t)p.ctas * 2 * 4 * S::kPartFloats;
+    p.rec = reinterpret_cast<SplitRec *>(at);
+    at += (size_t)p.ctas * sizeof(SplitRec);
+    p.failed = reinterpret_cast<uint32_t *>(at);
+    p.wait_limit_ns = wait_limit_ns();
+    p.debug_flags = debug_flags();
+    CUtensorMap q_map, k_map, v_map;
+    const uint64_t q_size[3] = {D, a.q_heads, kv.n_tokens}, q_stride[3] = {1, a.q_stride[1], a.q_stride[0]};
+    const uint32_t q_box[3] = {64, p.group, p.tile_tokens};
+    const uint64_t size[4] = {D, kv.page_tokens, kv.heads, kv.n_pages};
+    const uint64_t k_stride[4] = {1, kv.k_stride[2], kv.k_stride[1], kv.k_stride[0]};
+    const uint64_t v_stride[4] = {1, kv.v_stride[2], kv.v_stride[1], kv.v_stride[0]};
+    const uint32_t box[4] = {64, p.box_tokens, 1, 1};
+    if (!encode_tiled() || !make_map(&q_map, kv.dtype, const_cast<void *>(a.d_q), 3, q_size, q_stride, q_box) ||
+        !make_map(&k_map, kv.dtype, kv.d_k, 4, size, k_stride, box) || !make_map(&v_map, kv.dtype, kv.d_v, 4, size, v_stride, box))
+        return cudaErrorInvalidValue;
+    if (const cudaError_t e = allow_shared<attention_kernel<T, D, kM>>(S::kSmem)) return e;
+    attention_kernel<T, D, kM><<<p.ctas, S::kThreads, S::kSmem, s>>>(p, q_map, k_map, v_map);
+    if (const cudaError_t e = cudaGetLastError()) return e;
+    return launch_after(attention_join_kernel<T, D, kM>, dim3(p.ctas, kJoinY), dim3(kJoinThreads), 0, s, p, status);
+}
+
+template <typename T>
+static cudaError_t launch_attention_t(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, void *ws, const DeviceInfo &dev,
+                                      cudaStream_t s) {
+    if (!tensor_shape(kv, a)) return launch_any_t<T>(kv, a, status, s);
+    // Two row tiles per CTA share a key tile; with no more rows per request
+    // than one tile holds (on average: the lengths are on the device), two
+    // CTAs per SM of one row tile each keep more copies in flight.
+    const uint64_t rows = kv.n_tokens * (a.q_heads / kv.heads);
+    const bool two = rows > (uint64_t)kv.n_reqs * kTileRows;
+    if (kv.head_dim == 128)
+        return two ? launch_tensor<T, 128, 2>(kv, a, status, ws, dev, s) : launch_tensor<T, 128, 1>(kv, a, status, ws, dev, s);
+    return two ? launch_tensor<T, 64, 2>(kv, a, status, ws, dev, s) : launch_tensor<T, 64, 1>(kv, a, status, ws, dev, s);
+}
+
+cudaError_t launch_attention(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, void *ws, const DeviceInfo &dev,
+                             cudaStream_t s) {
+    return kv.dtype == SZ_BF16 ? launch_attention_t<__nv_bfloat16>(kv, a, status, ws, dev, s)
+                               : launch_attention_t<__half>(kv, a, status, ws, dev, s);
 }
 
 }  // namespace sz

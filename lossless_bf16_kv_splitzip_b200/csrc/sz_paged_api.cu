@@ -6,12 +6,15 @@
 namespace sz {
 
 cudaError_t launch_append(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, cudaStream_t s);
-cudaError_t launch_attention(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, cudaStream_t s);
+cudaError_t launch_attention(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, void *ws, const DeviceInfo &dev,
+                             cudaStream_t s);
+uint64_t attention_workspace(uint32_t head_dim);
 
 namespace {
 
-constexpr uint64_t kMaxRows = 0x7FFFFFFFull;    // row numbers are int32
-constexpr uint64_t kMaxStride = 1ull << 39;     // elements: a tensor map's strides are below 2^40 bytes
+constexpr uint64_t kMaxRows = 1ull << 30;       // rows, requests and positions: sums of two fit in an int32
+constexpr uint64_t kMaxPages = 0x7FFFFFFFull;   // page numbers are int32
+constexpr uint64_t kMaxStride = 1ull << 39;     // elements: a tensor map's strides stay below 2^40 bytes
 constexpr uint32_t kMaxHeads = 65535;           // a grid dimension
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -57,8 +60,8 @@ static sz_status check_out_rows(const sz_paged_kv *kv, const void *p, const uint
 
 sz_status check_paged_kv(const sz_paged_kv *kv) {
     if (!kv) return SZ_ERR_NULL;
-    if (kv->n_reqs > kMaxRows || kv->n_tokens > kMaxRows || kv->n_pages > kMaxRows) return SZ_ERR_TOO_LARGE;
-    if ((uint64_t)kv->max_pages * kv->page_tokens > kMaxRows) return SZ_ERR_TOO_LARGE;  // positions are int32
+    if (kv->n_reqs > kMaxRows || kv->n_tokens > kMaxRows || kv->n_pages > kMaxPages) return SZ_ERR_TOO_LARGE;
+    if (kv->page_tokens > kMaxRows || (uint64_t)kv->max_pages * kv->page_tokens > kMaxRows) return SZ_ERR_TOO_LARGE;
     if (kv->dtype != SZ_BF16 && kv->dtype != SZ_FP16) return SZ_ERR_INVALID;
     if (kv->heads == 0 || kv->heads > kMaxHeads || kv->page_tokens == 0) return SZ_ERR_INVALID;
     if (kv->head_dim == 0 || kv->head_dim > 256 || kv->head_dim % 8) return SZ_ERR_INVALID;
@@ -107,7 +110,7 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *a, int32_t *
 sz_status sz_plan_attention(uint32_t head_dim, uint64_t *workspace_bytes) {
     if (!workspace_bytes) return SZ_ERR_NULL;
     if (head_dim == 0 || head_dim > 256 || head_dim % 8) return SZ_ERR_INVALID;
-    *workspace_bytes = 256;
+    *workspace_bytes = attention_workspace(head_dim);
     return SZ_OK;
 }
 
@@ -125,7 +128,9 @@ sz_status sz_paged_attention(const sz_paged_kv *kv, const sz_attention_args *a, 
     uint64_t need = 0;
     if (const sz_status st = sz_plan_attention(kv->head_dim, &need)) return st;
     if (ws_bytes < need) return SZ_ERR_WORKSPACE;
-    const cudaError_t e = launch_attention(*kv, *a, d_status, static_cast<cudaStream_t>(stream));
+    DeviceInfo dev;
+    if (const sz_status st = device_info(dev)) return st;
+    const cudaError_t e = launch_attention(*kv, *a, d_status, d_ws, dev, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SZ_OK : SZ_ERR_CUDA;
 }
 
