@@ -148,6 +148,7 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
+constexpr int kPolyEvery = 4;  // every so many pairs of weights take the polynomial
 constexpr uint64_t kMinUnits = 1;                       // least share of a CTA
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
@@ -157,7 +158,11 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
     static constexpr int kSoftmaxThreads = kM * 128;
-    static constexpr int kThreads = kSoftmaxThreads + 64;
+    static constexpr int kThreads = kSoftmaxThreads + 128;
+    // registers a thread: softmax warps hold a row of scores, the others next
+    // to nothing.  Launched with 168 (three warpgroups) or 128 (two, twice
+    // per SM): 2 * 216 + 72 = 3 * 168, 184 + 72 = 2 * 128.
+    static constexpr int kManyRegs = kM == 2 ? 216 : 184, kFewRegs = 72;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
     static constexpr uint32_t kSmem = 1024 + kM * kTileBytes + kSlots * kTileBytes;
@@ -409,16 +414,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xFFFFFFFFu, ok) != 0;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 struct Bars {
     uint64_t full[10], empty[10];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2][2], pv_done[2];
     uint64_t drain;
 };
 
@@ -450,7 +449,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         mbar_init(&bars.q_empty, 1);
         for (int x = 0; x < kM; ++x) {
             mbar_init(&bars.s_full[x], 1);
-            mbar_init(&bars.p_full[x], 4);
+            mbar_init(&bars.p_full[x][0], 4);
+            mbar_init(&bars.p_full[x][1], 4);
             mbar_init(&bars.pv_done[x], 1);
         }
         mbar_init(&bars.drain, 1);
@@ -486,8 +486,9 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     volatile uint32_t *const fail = &failed;
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
-
-    if (wid == kCopyWarp) {
+    if (wid >= kMmaWarp) {
+        give_registers<S::kFewRegs>();
+        if (wid == kCopyWarp) {
         // ------------------------------------------------------------ copies
         const bool silent = (p.debug_flags & kDebugNoSignal) != 0;
         const uint32_t my_copy = lane / S::kHalves, my_half = lane % S::kHalves;
@@ -558,7 +559,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             for (uint32_t u = from; u < use; ++u) mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
             if (pieces) mbar_wait(&bars.q_full, (pieces - 1) & 1, limit);
         }
-    } else if (wid == kMmaWarp) {
+        } else if (wid == kMmaWarp) {
         // ---------------------------------------------------------- products
         uint32_t done[2] = {0, 0};  // score products per row tile
         uint32_t g = 0, pieces = 0;
@@ -625,16 +626,21 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             __syncwarp();
                         }
                     }
-                    if (!(ok = warp_wait(&bars.p_full[m], (done[m] - 1) & 1, fail, limit))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+                    for (int part = 0; part < 2 && ok; ++part) {  // the weights of 64 keys each
+                        if (!(ok = warp_wait(&bars.p_full[m][part], (done[m] - 1) & 1, fail, limit))) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
 #pragma unroll
-                        for (int i = 0; i < (int)kTileRows / 16; ++i)
-                            mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, operand_desc(vb + i * 16 * kRowBytes, kHalfBytes), kOutWord,
-                                     (t > w.t0 || i > 0) ? 1u : 0u);
-                        mma_commit(&bars.pv_done[m]);
+                            for (int k = 0; k < (int)kTileRows / 32; ++k) {
+                                const int i = part * ((int)kTileRows / 32) + k;
+                                mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, operand_desc(vb + i * 16 * kRowBytes, kHalfBytes), kOutWord,
+                                         (t > w.t0 || i > 0) ? 1u : 0u);
+                            }
+                            if (part == 1) mma_commit(&bars.pv_done[m]);
+                        }
                     }
+                    if (!ok) break;
                 }
                 if (more && active(nw, m)) {
                     if (!k_ready) {
@@ -670,8 +676,10 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             }
             __syncwarp();
         }
+        }
     } else {
         // ----------------------------------------------------------- softmax
+        take_registers<S::kManyRegs>();
         const uint32_t m_tile = wid / 4;
         const uint32_t row = tid & 127;
         const uint32_t lanes = (wid & 3) * 32;  // this warp's lanes of tensor memory
@@ -709,10 +717,10 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                     }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 32; j += 2)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(s[i][j]));
-                    const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
+                    const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     if (t == w.t0) {
                         m = high;
                     } else {
@@ -737,26 +745,42 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         }
                     }
                     const float ref = m == -INFINITY ? 0.0f : m * p.c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
+                    uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w16[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float a = exp2_fast(fmaf(__uint_as_float(s[i][2 * j]), p.c, -ref));
-                            const float b = exp2_fast(fmaf(__uint_as_float(s[i][2 * j + 1]), p.c, -ref));
-                            sum[i] += a;
-                            sum[(i + 1) & 3] += b;
-                            w16[j] = Half2<T>::narrow(a, b);
+                            const uint64_t x = fma2(pack2(__uint_as_float(s[i][2 * j]), __uint_as_float(s[i][2 * j + 1])), c2, ref2);
+                            uint64_t e;
+                            if (j % kPolyEvery == kPolyEvery - 1) {
+                                e = exp2_poly2(x);
+                            } else {
+                                const float2 f = unpack2(x);
+                                e = pack2(exp2_fast(f.x), exp2_fast(f.y));
+                            }
+                            sum[j & 1] = add2(sum[j & 1], e);
+                            const float2 f = unpack2(e);
+                            w16[j] = Half2<T>::narrow(f.x, f.y);
                         }
                         tmem_st16(s_at + i * 16, w16);
+                        if (i == 1) {  // the first half can go
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 both = unpack2(add2(sum[0], sum[1]));
+                    l = both.x + both.y;
                     tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(&bars.p_full[m_tile][0]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[m_tile]);
+                if (lane == 0) mbar_arrive(&bars.p_full[m_tile][1]);
             }
             if (!ok || !(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
             tc_fence_after();

@@ -102,4 +102,84 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// --------------------------------------------------- registers and arithmetic
+// Warpgroups of 4 warps trade registers; the shares add up to what the block
+// was launched with.
+template <int kCount>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+template <int kCount>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+
+// Two 32-bit numbers in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x of two numbers at most 128, without the special-function unit (16
+// results a clock and SM, which a softmax of tensor-core scores outruns).
+// x = i + f with i the nearest integer (Cody and Waite's reduction, by adding
+// and taking away 1.5 * 2^23); 2^f on [-1/2, 1/2] by the degree-5 polynomial
+// with constant term 1 whose largest relative error is least (linear
+// programme over 4,001 Chebyshev points: 8e-8; 1.6e-7 as evaluated in 32
+// bits); 2^i by its exponent field.  x is held at or above -127, where f = 0
+// and the exponent field 0 give exactly 0; a NaN stays a NaN.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
+    const float2 x = unpack2(x2);
+    x2 = pack2(max_nan(x.x, -127.0f), max_nan(x.y, -127.0f));
+    const uint64_t magic = pack2(12582912.0f, 12582912.0f), back = pack2(-12582912.0f, -12582912.0f);
+    const uint64_t t = add2(x2, magic);
+    const uint64_t f = fma2(add2(t, back), pack2(-1.0f, -1.0f), x2);
+    uint64_t p = pack2(0.0013274633092805743f, 0.0013274633092805743f);
+    p = fma2(p, f, pack2(0.009671961888670921f, 0.009671961888670921f));
+    p = fma2(p, f, pack2(0.055506784468889236f, 0.055506784468889236f));
+    p = fma2(p, f, pack2(0.24022234976291656f, 0.24022234976291656f));
+    p = fma2(p, f, pack2(0.6931470632553101f, 0.6931470632553101f));
+    p = fma2(p, f, pack2(1.0f, 1.0f));
+    const float2 ti = unpack2(t);
+    const float s0 = __uint_as_float((__float_as_uint(ti.x) << 23) + 0x3F800000u);
+    const float s1 = __uint_as_float((__float_as_uint(ti.y) << 23) + 0x3F800000u);
+    return mul2(p, pack2(s0, s1));
+}
+
 }  // namespace sz
