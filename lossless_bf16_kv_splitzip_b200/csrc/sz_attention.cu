@@ -148,7 +148,10 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
-constexpr int kPolyEvery = 4;  // every so many pairs of weights take the polynomial
+#ifndef SZ_POLY
+#define SZ_POLY 4
+#endif
+constexpr int kPolyEvery = SZ_POLY;  // every so many pairs of weights take the polynomial
 constexpr uint64_t kMinUnits = 1;                       // least share of a CTA
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
@@ -434,7 +437,10 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     __shared__ PlanShared plan;
     __shared__ uint32_t tmem_base_s;
     __shared__ uint32_t failed;
-    const uint32_t tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+    // what is the same for a whole warp is passed through a shuffle, so that
+    // the compiler keeps it in uniform registers, where the tensor
+    // instructions want their operands
+    const uint32_t tid = threadIdx.x, wid = same(tid >> 5), lane = tid & 31;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t ring0 = smem0 + kM * S::kTileBytes;
     constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1;
@@ -475,7 +481,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     allow_dependents();
-    const uint32_t tmem = tmem_base_s;
+    const uint32_t tmem = same(tmem_base_s);
     Cursor cur;
     cur.r = plan.r;
     cur.head = plan.head;
@@ -561,90 +567,98 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         }
         } else if (wid == kMmaWarp) {
         // ---------------------------------------------------------- products
+        const bool one = elect_one();
         uint32_t done[2] = {0, 0};  // score products per row tile
-        uint32_t g = 0, pieces = 0;
-        auto active = [&](const Piece &x, int m) {
-            return (uint32_t)x.q.n - x.block * kM * p.tile_tokens > (uint32_t)m * p.tile_tokens;
-        };
+        const uint32_t q_lo = desc_lo(smem0, 16), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
         auto slot_of = [&](uint32_t use) { return use % S::kSlots; };
-        auto score = [&](int m, uint32_t use) {  // S_m = Q_m K^T
-            if (lane == 0) {
-                const uint32_t qb = smem0 + m * S::kTileBytes, kb = ring0 + slot_of(use) * S::kTileBytes;
+        // tiles of the piece at hand: first, end, cached tokens, row tiles in use
+        int32_t t = 0, t_end = 0, kv = 0;
+        uint32_t tiles = 0;
+        auto take = [&](int32_t &a, int32_t &b, int32_t &c, uint32_t &m) -> bool {
+            const bool have = next_piece<kM>(p, cur, w);
+            a = (int32_t)same((uint32_t)w.t0);
+            b = (int32_t)same((uint32_t)w.t1);
+            c = (int32_t)same((uint32_t)w.q.kv);
+            m = same((kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens) ? 1u : 2u);
+            return same(have ? 1u : 0u) != 0;
+        };
+        auto score = [&](uint32_t m, uint32_t use) {  // S_m = Q_m K^T
+            const uint32_t a = q_lo + m * (S::kTileBytes >> 4), b = k_lo + slot_of(use) * (S::kTileBytes >> 4);
+            if (one) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = (uint32_t)(i / 4) * kHalfBytes + (uint32_t)(i % 4) * 32;
-                    mma_smem(tmem + m * 128, operand_desc(qb + off, 16), operand_desc(kb + off, 16), kScoreWord, i > 0);
+                    const uint32_t off = ((uint32_t)(i / 4) * kHalfBytes + (uint32_t)(i % 4) * 32) >> 4;
+                    mma_smem(tmem + m * 128, full_desc(a + off), full_desc(b + off), kScoreWord, i > 0);
                 }
                 mma_commit(&bars.s_full[m]);
             }
             ++done[m];
         };
-        bool ok = true;
-        bool have = next_piece<kM>(p, cur, w);
-        int32_t t = have ? w.t0 : 0;
+        bool have = take(t, t_end, kv, tiles);
+        bool ok = true, first = true;  // first: the piece's first tile
+        uint32_t g = 0, pieces = 0;
         if (have) {
             ok = warp_wait(&bars.q_full, 0, fail, limit) && warp_wait(&bars.full[0], 0, fail, limit);
             ++pieces;
             if (ok) {
                 tc_fence_after();
-                for (int m = 0; m < kM; ++m)
-                    if (active(w, m)) score(m, 0);
-                if (lane == 0) {
+                for (uint32_t m = 0; m < tiles; ++m) score(m, 0);
+                if (one) {
                     mma_commit(&bars.empty[0]);
-                    if (w.t0 + 1 == w.t1) mma_commit(&bars.q_empty);
+                    if (t + 1 == t_end) mma_commit(&bars.q_empty);
                 }
             }
         }
         while (have && ok) {
-            Piece nw = w;
-            int32_t nt = t + 1;
-            bool more = true;
-            if (nt >= w.t1) {
-                more = next_piece<kM>(p, cur, nw);
-                nt = nw.t0;
+            int32_t nt = t + 1, nt_end = t_end, nkv = kv;
+            uint32_t ntiles = tiles;
+            bool more = true, nfirst = false;
+            if (nt >= t_end) {
+                more = take(nt, nt_end, nkv, ntiles);
+                nfirst = true;
+                if (!more) ntiles = 0;
             }
             const uint32_t vu = 2 * g + 1, ku = 2 * g + 2;
-            bool v_ready = false, k_ready = false;
+            if (!(ok = warp_wait(&bars.full[slot_of(vu)], vu / S::kSlots & 1, fail, limit))) break;
             // keys behind the last token in this tile's last page: their
             // weights are 0, so their values must be finite
-            const int32_t z0 = w.q.kv - t * (int32_t)p.key_tile;
-            for (int m = 0; m < kM && ok; ++m) {
-                if (active(w, m)) {
-                    if (!v_ready) {
-                        if (!(ok = warp_wait(&bars.full[slot_of(vu)], vu / S::kSlots & 1, fail, limit))) break;
-                        v_ready = true;
-                        if (z0 > 0 && z0 < (int32_t)p.key_tile) {
-                            const int32_t page = (int32_t)p.kv.page_tokens;
-                            const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)w.q.kv + page - 1) / page * page - (int64_t)t * p.key_tile);
-                            const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
-                            for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
-                                const uint32_t piece = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0)
-                                             : "memory");
-                            }
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                        }
-                    }
-                    for (int part = 0; part < 2 && ok; ++part) {  // the weights of 64 keys each
+            const int32_t z0 = kv - t * (int32_t)p.key_tile;
+            if (z0 > 0 && z0 < (int32_t)p.key_tile) {
+                const int32_t page = (int32_t)p.kv.page_tokens;
+                const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
+                const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+                for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
+                    const uint32_t piece = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0)
+                                 : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            bool k_ready = false;
+            const uint32_t vb = v_lo + slot_of(vu) * (S::kTileBytes >> 4);
+            const uint32_t most = kM == 1 ? 1u : max(tiles, ntiles);
+            for (uint32_t m = 0; m < most; ++m) {
+                if (m < tiles) {
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {  // the weights of 64 keys each
                         if (!(ok = warp_wait(&bars.p_full[m][part], (done[m] - 1) & 1, fail, limit))) break;
                         tc_fence_after();
-                        if (lane == 0) {
-                            const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+                        if (one) {
 #pragma unroll
                             for (int k = 0; k < (int)kTileRows / 32; ++k) {
                                 const int i = part * ((int)kTileRows / 32) + k;
-                                mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, operand_desc(vb + i * 16 * kRowBytes, kHalfBytes), kOutWord,
-                                         (t > w.t0 || i > 0) ? 1u : 0u);
+                                mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, full_desc(vb + i * (16 * kRowBytes >> 4)), kOutWord,
+                                         (!first || i > 0) ? 1u : 0u);
                             }
                             if (part == 1) mma_commit(&bars.pv_done[m]);
                         }
                     }
                     if (!ok) break;
                 }
-                if (more && active(nw, m)) {
+                if (m < ntiles) {
                     if (!k_ready) {
-                        if (nt == nw.t0) {
+                        if (nfirst) {
                             if (!(ok = warp_wait(&bars.q_full, pieces & 1, fail, limit))) break;
                             ++pieces;
                         }
@@ -656,21 +670,23 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 }
             }
             if (!ok) break;
-            if (lane == 0) {
+            if (one) {
                 mma_commit(&bars.empty[slot_of(vu)]);
                 if (more) {
                     mma_commit(&bars.empty[slot_of(ku)]);
-                    if (nt + 1 == nw.t1) mma_commit(&bars.q_empty);
+                    if (nt + 1 == nt_end) mma_commit(&bars.q_empty);
                 }
             }
-            __syncwarp();
-            w = nw;
             t = nt;
+            t_end = nt_end;
+            kv = nkv;
+            tiles = ntiles;
             have = more;
+            first = nfirst;
             ++g;
         }
         if (!ok) {  // products under way must end before their memory is given back
-            if (lane == 0) {
+            if (one) {
                 mma_commit(&bars.drain);
                 mbar_wait(&bars.drain, 0, limit);
             }
@@ -700,6 +716,89 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 if (!(ok = warp_wait(&bars.s_full[m_tile], n & 1, fail, limit))) break;
                 tc_fence_after();
                 if (warp_live) {
+#ifdef SZ_REREAD
+                    const int32_t k0 = t * (int32_t)p.key_tile;
+                    const int32_t from = max(begin - k0, 0), to = min(stop - k0, (int32_t)p.key_tile);
+                    const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows) != 0;
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    {
+                        uint32_t s[4][32];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s[i]);
+                        tmem_wait_ld();
+                        if (masked)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (i * 32 + j < from || i * 32 + j >= to) s[i][j] = 0xFF800000u;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
+                    }
+                    const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+                    if (t == w.t0) {
+                        m = high;
+                    } else {
+                        const bool rise = (high - m) * p.c > kRescaleAt;
+                        if (__any_sync(0xFFFFFFFFu, rise)) {
+                            // the accumulator as of the tile before
+                            if (!(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
+                            tc_fence_after();
+                            const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
+                            if (rise) m = high;
+                            l *= f;
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + i * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st32(o_at + i * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
+                    const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
+                    uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t s[32], w16[16];
+                        tmem_ld32(s_at + i * 32, s);
+                        tmem_wait_ld();
+                        if (masked)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (i * 32 + j < from || i * 32 + j >= to) s[j] = 0xFF800000u;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, ref2);
+                            uint64_t e;
+                            if (j % kPolyEvery == kPolyEvery - 1) {
+                                e = exp2_poly2(x);
+                            } else {
+                                const float2 f = unpack2(x);
+                                e = pack2(exp2_fast(f.x), exp2_fast(f.y));
+                            }
+                            sum[j & 1] = add2(sum[j & 1], e);
+                            const float2 f = unpack2(e);
+                            w16[j] = Half2<T>::narrow(f.x, f.y);
+                        }
+                        tmem_st16(s_at + i * 16, w16);
+                        if (i == 1) {  // the first half can go
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
+                        }
+                    }
+                    const float2 both = unpack2(add2(sum[0], sum[1]));
+                    l = both.x + both.y;
+                    tmem_wait_st();
+#else
                     uint32_t s[4][32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s[i]);
@@ -775,6 +874,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                     const float2 both = unpack2(add2(sum[0], sum[1]));
                     l = both.x + both.y;
                     tmem_wait_st();
+#endif
                 } else if (lane == 0) {
                     mbar_arrive(&bars.p_full[m_tile][0]);
                 }

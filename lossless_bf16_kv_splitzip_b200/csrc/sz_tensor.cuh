@@ -26,6 +26,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const CUtensorMap
         : "memory");
 }
 
+// A value all lanes of the warp hold, and one lane of a converged warp, in a
+// form that the compiler knows to be uniform.
+__device__ __forceinline__ uint32_t same(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ------------------------------------------------------------ tensor memory
 // Both by one whole warp; columns a power of two >= 32.
 __device__ __forceinline__ void tmem_alloc(uint32_t *smem_dst, uint32_t columns) {
@@ -76,9 +85,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
 // tensor-map copy's 128-byte mode lays them (1,024-byte aligned tiles).
 // `lead`: bytes between 64-value blocks along the contiguous dimension
 // (used when that is not the reduced one); groups of 8 lie 1,024 apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t smem, uint32_t lead) {
-    return (uint64_t)((smem & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
+// Only the low word depends on the address: 16-byte steps add to it.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem, uint32_t lead) { return (smem & 0x3FFFFu) >> 4 | (lead >> 4) << 16; }
+__device__ __forceinline__ uint64_t full_desc(uint32_t lo) {
+    constexpr uint64_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return kHigh << 32 | lo;
 }
 // Instruction word of a 16-bit product with 32-bit sums, m = 128 rows.
 __host__ __device__ constexpr uint32_t mma_word(bool bf16, uint32_t n, bool b_row_contiguous) {
