@@ -161,11 +161,7 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
     static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
     static constexpr int kSoftmaxThreads = kM * 128;
-    static constexpr int kThreads = kSoftmaxThreads + 128;
-    // registers a thread: softmax warps hold a row of scores, the others next
-    // to nothing.  Launched with 168 (three warpgroups) or 128 (two, twice
-    // per SM): 2 * 216 + 72 = 3 * 168, 184 + 72 = 2 * 128.
-    static constexpr int kManyRegs = kM == 2 ? 216 : 184, kFewRegs = 72;
+    static constexpr int kThreads = kSoftmaxThreads + 96;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
     static constexpr uint32_t kSmem = 1024 + kM * kTileBytes + kSlots * kTileBytes;
@@ -402,8 +398,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
 // Wait for a phase, by all lanes of a warp: false when the limit of device
 // time ran out here or elsewhere in the CTA.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    bool ok = false;
-    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
         const uint64_t t0 = globaltimer_ns();
         while (!(ok = mbar_try_wait(bar, parity))) {
@@ -415,6 +410,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
         }
     }
     return __all_sync(0xFFFFFFFFu, ok) != 0;
+}
+
+// The same for a role whose accesses stay in bounds whatever the data: it
+// goes on after a failure, which ends all further waits at once.
+__device__ __forceinline__ void wait_or_fail(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) break;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            *failed = 1u;
+            break;
+        }
+    }
+}
+
+// Columns outside [from, to) of 64 scores become -inf.
+__device__ __forceinline__ void hide(uint32_t (&s)[64], int32_t from, int32_t to) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+        if (j < from || j >= to) s[j] = 0xFF800000u;
 }
 
 struct Bars {
@@ -443,7 +459,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint32_t tid = threadIdx.x, wid = same(tid >> 5), lane = tid & 31;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t ring0 = smem0 + kM * S::kTileBytes;
-    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1;
+    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1;  // and the one after it
 
     if (wid == kMmaWarp) tmem_alloc(&tmem_base_s, S::kColumns);
     if (tid == 0) {
@@ -493,15 +509,15 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
     if (wid >= kMmaWarp) {
-        give_registers<S::kFewRegs>();
-        if (wid == kCopyWarp) {
-        // ------------------------------------------------------------ copies
+        if (wid >= kCopyWarp) {
+        // ------------------------------------- copies: Q and K, or V
+        const bool one = elect_one();
+        const uint32_t is_v = wid - kCopyWarp;
+        const CUtensorMap *const map = is_v ? &v_map : &k_map;
         const bool silent = (p.debug_flags & kDebugNoSignal) != 0;
-        const uint32_t my_copy = lane / S::kHalves, my_half = lane % S::kHalves;
-        const bool mine = my_copy < p.copies;
         const uint32_t tile_bytes = p.key_tile * S::kHalves * kRowBytes;
-        const uint32_t dst_off = my_half * kHalfBytes + my_copy * p.box_tokens * kRowBytes;
-        uint32_t use = 0, pieces = 0;  // ring uses, pieces begun
+        const uint32_t copy_bytes = p.box_tokens * kRowBytes;
+        uint32_t use = is_v, pieces = 0;  // of the ring (K even, V odd), pieces begun
         bool ok = true;
         SplitRec rec;
         rec.r = rec.head = rec.block = rec.last = 0;
@@ -519,16 +535,21 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             const uint32_t first = w.block * kM * p.tile_tokens;
             const uint32_t tokens = umin32((uint32_t)w.q.n - first, kM * p.tile_tokens);
             const uint32_t tiles = kM == 1 || tokens <= p.tile_tokens ? 1u : 2u;
-            if (!(ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, fail, limit))) break;
-            ++pieces;
-            if (lane == 0) {
-                const uint32_t rows = p.tile_tokens * p.group;
-                mbar_arrive_expect_tx(&bars.q_full, tiles * rows * S::kHalves * kRowBytes);
-                if (!silent)
-                    for (uint32_t x = 0; x < tiles; ++x)
-                        for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
-                            tma_load_3d(smem0 + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(w.head * p.group),
-                                        (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full));
+            const uint32_t head = same(w.head);
+            if (!is_v) {
+                if (!(ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, fail, limit))) break;
+                ++pieces;
+                if (one) {
+                    const uint32_t rows = p.tile_tokens * p.group;
+                    mbar_arrive_expect_tx(&bars.q_full, tiles * rows * S::kHalves * kRowBytes);
+                    if (!silent)
+                        for (uint32_t x = 0; x < tiles; ++x)
+#pragma unroll
+                            for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
+                                tma_load_3d(smem0 + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(head * p.group),
+                                            (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full));
+                }
+                __syncwarp();
             }
             int32_t begin, stop;
             key_range(p, w.q, (int32_t)first, (int32_t)(first + tokens), &begin, &stop);
@@ -537,32 +558,37 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             // Pages behind the last token, before the window or outside the
             // pool are copied from behind the pool's end: zeros.
             auto page_at = [&](int32_t t) -> int32_t {
-                const int32_t i = t * (int32_t)p.key_tile / (int32_t)p.kv.page_tokens + (int32_t)my_copy;
+                const int32_t i = t * (int32_t)p.key_tile / (int32_t)p.kv.page_tokens + (int32_t)lane;
                 int32_t page = -1;
-                if (mine && i >= page_lo && i < page_hi) page = page_of(p.kv, w.r, (uint32_t)i);
+                if (lane < p.copies && i >= page_lo && i < page_hi) page = page_of(p.kv, w.r, (uint32_t)i);
                 return page < 0 ? (int32_t)p.kv.n_pages : page;
             };
             int32_t page = page_at(w.t0);
-            for (int32_t t = w.t0; t < w.t1 && ok; ++t) {
-                const int32_t slot_tok = p.box_tokens < p.kv.page_tokens ? t * (int32_t)p.key_tile % (int32_t)p.kv.page_tokens : 0;
-                const int32_t next = t + 1 < w.t1 ? page_at(t + 1) : 0;
-                for (int kv2 = 0; kv2 < 2; ++kv2) {
-                    const uint32_t slot = use % S::kSlots, phase = use / S::kSlots & 1;
-                    if (!(ok = warp_wait(&bars.empty[slot], phase ^ 1, fail, limit))) break;
-                    ++use;
-                    if (lane == 0) mbar_arrive_expect_tx(&bars.full[slot], tile_bytes);
-                    __syncwarp();
-                    if (mine && !silent)
-                        tma_load_4d(ring0 + slot * S::kTileBytes + dst_off, kv2 ? &v_map : &k_map, (int)(my_half * 64), slot_tok,
-                                    (int)w.head, page, smem_u32(&bars.full[slot]));
+            const int32_t t_end = (int32_t)same((uint32_t)w.t1);
+            for (int32_t t = (int32_t)same((uint32_t)w.t0); t < t_end; ++t, use += 2) {
+                const int32_t token = p.box_tokens < p.kv.page_tokens ? t * (int32_t)p.key_tile % (int32_t)p.kv.page_tokens : 0;
+                const uint32_t slot = use % S::kSlots, phase = use / S::kSlots & 1;
+                if (!(ok = warp_wait(&bars.empty[slot], phase ^ 1, fail, limit))) break;
+                const uint32_t bar = smem_u32(&bars.full[slot]);
+                if (one) mbar_arrive_expect_tx(&bars.full[slot], tile_bytes);
+                uint32_t dst = ring0 + slot * S::kTileBytes;
+                for (uint32_t i = 0; i < p.copies; ++i, dst += copy_bytes) {
+                    const int32_t from = (int32_t)__shfl_sync(0xFFFFFFFFu, page, i);
+                    if (one && !silent) {
+#pragma unroll
+                        for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
+                            tma_load_4d(dst + hf * kHalfBytes, map, (int)(hf * 64), token, (int)head, from, bar);
+                    }
                 }
-                page = next;
+                __syncwarp();
+                if (t + 1 < t_end) page = page_at(t + 1);
             }
         }
-        if (lane == 0) p.rec[blockIdx.x] = rec;
+        if (is_v && lane == 0) p.rec[blockIdx.x] = rec;
         if (!ok && !silent) {  // copies still under way must land before the CTA ends
-            const uint32_t from = use > (uint32_t)S::kSlots ? use - S::kSlots : 0;
-            for (uint32_t u = from; u < use; ++u) mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
+            // (this warp's uses of the last round of slots)
+            for (uint32_t u = use > 2 * S::kSlots ? use - 2 * S::kSlots : is_v; u < use; u += 2)
+                mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
             if (pieces) mbar_wait(&bars.q_full, (pieces - 1) & 1, limit);
         }
         } else if (wid == kMmaWarp) {
@@ -570,7 +596,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         const bool one = elect_one();
         uint32_t done[2] = {0, 0};  // score products per row tile
         const uint32_t q_lo = desc_lo(smem0, 16), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
-        auto slot_of = [&](uint32_t use) { return use % S::kSlots; };
         // tiles of the piece at hand: first, end, cached tokens, row tiles in use
         int32_t t = 0, t_end = 0, kv = 0;
         uint32_t tiles = 0;
@@ -582,8 +607,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             m = same((kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens) ? 1u : 2u);
             return same(have ? 1u : 0u) != 0;
         };
-        auto score = [&](uint32_t m, uint32_t use) {  // S_m = Q_m K^T
-            const uint32_t a = q_lo + m * (S::kTileBytes >> 4), b = k_lo + slot_of(use) * (S::kTileBytes >> 4);
+        auto score = [&](uint32_t m, uint32_t at) {  // S_m = Q_m K^T
+            const uint32_t a = q_lo + m * (S::kTileBytes >> 4), b = k_lo + at * (S::kTileBytes >> 4);
             if (one) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -592,24 +617,26 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 }
                 mma_commit(&bars.s_full[m]);
             }
+            __syncwarp();
             ++done[m];
         };
         bool have = take(t, t_end, kv, tiles);
-        bool ok = true, first = true;  // first: the piece's first tile
-        uint32_t g = 0, pieces = 0;
+        bool first = true;  // the piece's first tile
+        uint32_t pieces = 0, slot = 1 % S::kSlots, phase = 0;  // of the ring, at this tile's V
         if (have) {
-            ok = warp_wait(&bars.q_full, 0, fail, limit) && warp_wait(&bars.full[0], 0, fail, limit);
+            wait_or_fail(&bars.q_full, 0, fail, limit);
+            wait_or_fail(&bars.full[0], 0, fail, limit);
             ++pieces;
-            if (ok) {
-                tc_fence_after();
-                for (uint32_t m = 0; m < tiles; ++m) score(m, 0);
-                if (one) {
-                    mma_commit(&bars.empty[0]);
-                    if (t + 1 == t_end) mma_commit(&bars.q_empty);
-                }
+            tc_fence_after();
+#pragma unroll
+            for (uint32_t m = 0; m < kM; ++m)
+                if (m < tiles) score(m, 0);
+            if (one) {
+                mma_commit(&bars.empty[0]);
+                if (t + 1 == t_end) mma_commit(&bars.q_empty);
             }
         }
-        while (have && ok) {
+        while (have && *fail == 0) {
             int32_t nt = t + 1, nt_end = t_end, nkv = kv;
             uint32_t ntiles = tiles;
             bool more = true, nfirst = false;
@@ -618,15 +645,20 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 nfirst = true;
                 if (!more) ntiles = 0;
             }
-            const uint32_t vu = 2 * g + 1, ku = 2 * g + 2;
-            if (!(ok = warp_wait(&bars.full[slot_of(vu)], vu / S::kSlots & 1, fail, limit))) break;
+            // V of this tile and K of the next (and the next piece's Q) first, so
+            // that nothing is waited for between the weights and the products
+            const uint32_t v_slot = slot, k_slot = slot + 1 == S::kSlots ? 0 : slot + 1;
+            const uint32_t v_phase = phase, k_phase = phase ^ (k_slot == 0 ? 1u : 0u);
+            slot = k_slot + 1 == S::kSlots ? 0 : k_slot + 1;
+            phase = k_phase ^ (slot == 0 ? 1u : 0u);
+            wait_or_fail(&bars.full[v_slot], v_phase, fail, limit);
             // keys behind the last token in this tile's last page: their
             // weights are 0, so their values must be finite
             const int32_t z0 = kv - t * (int32_t)p.key_tile;
             if (z0 > 0 && z0 < (int32_t)p.key_tile) {
                 const int32_t page = (int32_t)p.kv.page_tokens;
                 const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
-                const uint32_t vb = ring0 + slot_of(vu) * S::kTileBytes;
+                const uint32_t vb = ring0 + v_slot * S::kTileBytes;
                 for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
                     const uint32_t piece = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
                     asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0)
@@ -635,45 +667,39 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
-            bool k_ready = false;
-            const uint32_t vb = v_lo + slot_of(vu) * (S::kTileBytes >> 4);
-            const uint32_t most = kM == 1 ? 1u : max(tiles, ntiles);
-            for (uint32_t m = 0; m < most; ++m) {
+            if (more) {
+                if (nfirst) {
+                    wait_or_fail(&bars.q_full, pieces & 1, fail, limit);
+                    ++pieces;
+                }
+                wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
+            }
+            const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
+#pragma unroll
+            for (uint32_t m = 0; m < kM; ++m) {
                 if (m < tiles) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {  // the weights of 64 keys each
-                        if (!(ok = warp_wait(&bars.p_full[m][part], (done[m] - 1) & 1, fail, limit))) break;
+                    for (uint32_t part = 0; part < 2; ++part) {  // the weights of 64 keys each
+                        wait_or_fail(&bars.p_full[m][part], (done[m] - 1) & 1, fail, limit);
                         tc_fence_after();
                         if (one) {
 #pragma unroll
-                            for (int k = 0; k < (int)kTileRows / 32; ++k) {
-                                const int i = part * ((int)kTileRows / 32) + k;
+                            for (uint32_t k = 0; k < kTileRows / 32; ++k) {
+                                const uint32_t i = part * (kTileRows / 32) + k;
                                 mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, full_desc(vb + i * (16 * kRowBytes >> 4)), kOutWord,
                                          (!first || i > 0) ? 1u : 0u);
                             }
                             if (part == 1) mma_commit(&bars.pv_done[m]);
                         }
+                        __syncwarp();
                     }
-                    if (!ok) break;
                 }
-                if (m < ntiles) {
-                    if (!k_ready) {
-                        if (nfirst) {
-                            if (!(ok = warp_wait(&bars.q_full, pieces & 1, fail, limit))) break;
-                            ++pieces;
-                        }
-                        if (!(ok = warp_wait(&bars.full[slot_of(ku)], ku / S::kSlots & 1, fail, limit))) break;
-                        k_ready = true;
-                        tc_fence_after();
-                    }
-                    score(m, ku);
-                }
+                if (m < ntiles) score(m, k_slot);
             }
-            if (!ok) break;
             if (one) {
-                mma_commit(&bars.empty[slot_of(vu)]);
+                mma_commit(&bars.empty[v_slot]);
                 if (more) {
-                    mma_commit(&bars.empty[slot_of(ku)]);
+                    mma_commit(&bars.empty[k_slot]);
                     if (nt + 1 == nt_end) mma_commit(&bars.q_empty);
                 }
             }
@@ -683,9 +709,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             tiles = ntiles;
             have = more;
             first = nfirst;
-            ++g;
         }
-        if (!ok) {  // products under way must end before their memory is given back
+        if (*fail) {  // products under way must end before their memory is given back
             if (one) {
                 mma_commit(&bars.drain);
                 mbar_wait(&bars.drain, 0, limit);
@@ -695,7 +720,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         }
     } else {
         // ----------------------------------------------------------- softmax
-        take_registers<S::kManyRegs>();
+
         const uint32_t m_tile = wid / 4;
         const uint32_t row = tid & 127;
         const uint32_t lanes = (wid & 3) * 32;  // this warp's lanes of tensor memory
@@ -703,54 +728,50 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D;
         const uint32_t my_token = row / p.group, my_head = row % p.group;
         uint32_t n = 0;  // tiles done by this row tile
-        bool ok = true;
-        while (ok && next_piece<kM>(p, cur, w)) {
+        while (next_piece<kM>(p, cur, w)) {
             const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
             if ((uint32_t)w.q.n <= first) continue;
             const uint32_t rows = umin32((uint32_t)w.q.n - first, p.tile_tokens) * p.group;
             const bool warp_live = lanes < rows;
             int32_t begin, stop;
             key_range(p, w.q, (int32_t)(first + my_token), (int32_t)(first + my_token) + 1, &begin, &stop);
-            float m = -INFINITY, l = 0.0f;  // reference of the weights, their sum
-            for (int32_t t = w.t0; t < w.t1; ++t, ++n) {
-                if (!(ok = warp_wait(&bars.s_full[m_tile], n & 1, fail, limit))) break;
+            float m = -INFINITY;             // reference of the weights
+            uint64_t sum = pack2(0.0f, 0.0f);  // of the weights, in two parts
+            int32_t k0 = w.t0 * (int32_t)p.key_tile;
+            for (int32_t t = w.t0; t < w.t1; ++t, ++n, k0 += (int32_t)p.key_tile) {
+                wait_or_fail(&bars.s_full[m_tile], n & 1, fail, limit);
                 tc_fence_after();
+                // this row's visible columns; the same for all rows of most tiles
+                const int32_t from = begin - k0, to = min(stop - k0, (int32_t)p.key_tile);
+                const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows) != 0;
+                float high = -INFINITY;
                 if (warp_live) {
-#ifdef SZ_REREAD
-                    const int32_t k0 = t * (int32_t)p.key_tile;
-                    const int32_t from = max(begin - k0, 0), to = min(stop - k0, (int32_t)p.key_tile);
-                    const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows) != 0;
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    {
-                        uint32_t s[4][32];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s[i]);
+#pragma unroll 1
+                    for (uint32_t half = 0; half < 2; ++half) {
+                        uint32_t s[64];
+                        tmem_ld64(s_at + half * 64, s);
                         tmem_wait_ld();
-                        if (masked)
+                        if (masked) hide(s, from - (int32_t)half * 64, to - (int32_t)half * 64);
+                        float top[4] = {high, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
+                        for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (i * 32 + j < from || i * 32 + j >= to) s[i][j] = 0xFF800000u;
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
+                            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]));
+                        high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     }
-                    const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     if (t == w.t0) {
                         m = high;
                     } else {
                         const bool rise = (high - m) * p.c > kRescaleAt;
                         if (__any_sync(0xFFFFFFFFu, rise)) {
                             // the accumulator as of the tile before
-                            if (!(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
+                            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
                             tc_fence_after();
                             const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
                             if (rise) m = high;
-                            l *= f;
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
+                            sum = mul2(sum, pack2(f, f));
+#pragma unroll 1
+                            for (uint32_t i = 0; i < D / 32; ++i) {
                                 uint32_t o[32];
                                 tmem_ld32(o_at + i * 32, o);
                                 tmem_wait_ld();
@@ -761,20 +782,22 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             tmem_wait_st();
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
-                    const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
-                    uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
+                }
+                const float ref = m == -INFINITY ? 0.0f : m * p.c;
+                const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t s[32], w16[16];
-                        tmem_ld32(s_at + i * 32, s);
+                for (uint32_t half = 0; half < 2; ++half) {
+                    if (warp_live) {
+                        // The scores are read again: tensor memory is close by,
+                        // and a row kept in registers costs more than that.
+                        // Weights of columns 64h .. take columns 32h ..
+                        uint32_t s[64];
+                        tmem_ld64(s_at + half * 64, s);
                         tmem_wait_ld();
-                        if (masked)
+                        if (masked) hide(s, from - (int32_t)half * 64, to - (int32_t)half * 64);
+                        uint64_t sum1 = pack2(0.0f, 0.0f);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (i * 32 + j < from || i * 32 + j >= to) s[j] = 0xFF800000u;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 32; ++j) {
                             const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, ref2);
                             uint64_t e;
                             if (j % kPolyEvery == kPolyEvery - 1) {
@@ -783,106 +806,22 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                                 const float2 f = unpack2(x);
                                 e = pack2(exp2_fast(f.x), exp2_fast(f.y));
                             }
-                            sum[j & 1] = add2(sum[j & 1], e);
+                            if (j & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
                             const float2 f = unpack2(e);
-                            w16[j] = Half2<T>::narrow(f.x, f.y);
+                            s[j] = Half2<T>::narrow(f.x, f.y);
                         }
-                        tmem_st16(s_at + i * 16, w16);
-                        if (i == 1) {  // the first half can go
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
-                        }
+                        sum = add2(sum, sum1);
+                        tmem_st32(s_at + half * 32, s);
+                        tmem_wait_st();
                     }
-                    const float2 both = unpack2(add2(sum[0], sum[1]));
-                    l = both.x + both.y;
-                    tmem_wait_st();
-#else
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(s_at + i * 32, s[i]);
-                    tmem_wait_ld();
-                    const int32_t k0 = t * (int32_t)p.key_tile;
-                    const int32_t from = max(begin - k0, 0), to = min(stop - k0, (int32_t)p.key_tile);
-                    if (__any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows)) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int32_t col = i * 32 + j;
-                                if (col < from || col >= to) s[i][j] = 0xFF800000u;  // -inf
-                            }
-                    }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1]));
-                    const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-                    if (t == w.t0) {
-                        m = high;
-                    } else {
-                        const bool rise = (high - m) * p.c > kRescaleAt;
-                        if (__any_sync(0xFFFFFFFFu, rise)) {
-                            // the accumulator as of the tile before
-                            if (!(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
-                            tc_fence_after();
-                            const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
-                            if (rise) m = high;
-                            l *= f;
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld32(o_at + i * 32, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st32(o_at + i * 32, o);
-                            }
-                            tmem_wait_st();
-                        }
-                    }
-                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
-                    const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
-                    uint64_t sum[2] = {pack2(l, 0.0f), pack2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w16[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const uint64_t x = fma2(pack2(__uint_as_float(s[i][2 * j]), __uint_as_float(s[i][2 * j + 1])), c2, ref2);
-                            uint64_t e;
-                            if (j % kPolyEvery == kPolyEvery - 1) {
-                                e = exp2_poly2(x);
-                            } else {
-                                const float2 f = unpack2(x);
-                                e = pack2(exp2_fast(f.x), exp2_fast(f.y));
-                            }
-                            sum[j & 1] = add2(sum[j & 1], e);
-                            const float2 f = unpack2(e);
-                            w16[j] = Half2<T>::narrow(f.x, f.y);
-                        }
-                        tmem_st16(s_at + i * 16, w16);
-                        if (i == 1) {  // the first half can go
-                            tmem_wait_st();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
-                        }
-                    }
-                    const float2 both = unpack2(add2(sum[0], sum[1]));
-                    l = both.x + both.y;
-                    tmem_wait_st();
-#endif
-                } else if (lane == 0) {
-                    mbar_arrive(&bars.p_full[m_tile][0]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.p_full[m_tile][half]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[m_tile][1]);
             }
-            if (!ok || !(ok = warp_wait(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit))) break;
+            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
+            const float2 both = unpack2(sum);
+            const float l = both.x + both.y;
             tc_fence_after();
             if (!warp_live) continue;
             const bool mine = row < rows;
