@@ -5,6 +5,9 @@
 // to m' = max(m, s), l' = l e^(m - m') + e^(s - m'), o' = o e^(m - m') +
 // e^(s - m') v; two such triples over different keys join the same way.
 // Exponentials are taken base 2 of scores scaled by log2(e).
+#include <atomic>
+#include <chrono>
+#include <random>
 #include <type_traits>
 
 #include "sz_paged.cuh"
@@ -152,25 +155,40 @@ constexpr float kRescaleAt = 8.0f;
 #define SZ_POLY 4
 #endif
 constexpr int kPolyEvery = SZ_POLY;  // every so many pairs of weights take the polynomial
-constexpr uint64_t kMinUnits = 1;                       // least share of a CTA
+constexpr uint32_t kWholeTiles = 6;                     // blocks up to this long are not split when there is a CTA for each
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
 template <int D, int kM>
 struct Shape {
-    static constexpr int kHalves = D / 64;
+    static constexpr int kTiles = kM, kHalves = D / 64;
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
-    static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+    static constexpr int kQueries = D == 64 ? 2 : 1;  // blocks whose queries are in shared memory at a time
+    static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 4);
     static constexpr int kSoftmaxThreads = kM * 128;
-    static constexpr int kThreads = kSoftmaxThreads + 96;
+    static constexpr int kThreads = kSoftmaxThreads + 128;
+    // Registers a thread, traded between warpgroups: launched with 168 (three
+    // of them) or 128 (two, twice per SM); 2 * 208 + 88 = 3 * 168, 168 + 88 = 2 * 128.
+    static constexpr int kManyRegs = kM == 2 ? 208 : 168, kFewRegs = 88;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
-    static constexpr uint32_t kSmem = 1024 + kM * kTileBytes + kSlots * kTileBytes;
-    static constexpr uint32_t kPartFloats = kM * kTileRows * (D + 2);  // a block's rows, then (m, l) per row
+    static constexpr uint32_t kQueryBytes = kM * kTileBytes;
+    static constexpr uint32_t kSmem = 1024 + kQueries * kQueryBytes + kSlots * kTileBytes;
+    // A part of a block: per row tile 4 channels of all rows, the next 4, ...
+    // (so that threads that hold a row each write and read side by side),
+    // then (m, l) per row.
+    static constexpr uint32_t kPartFloats = kM * kTileRows * (D + 2);
+    static __host__ __device__ constexpr uint32_t part_o(uint32_t m_tile, uint32_t chunk, uint32_t row) {
+        return ((m_tile * (D / 4) + chunk) * kTileRows + row) * 4;
+    }
+    static __host__ __device__ constexpr uint32_t part_ml(uint32_t m_tile, uint32_t row) {
+        return kM * kTileRows * D + (m_tile * kTileRows + row) * 2;
+    }
 };
 
-// A block whose keys continue in the CTAs after the one that began it.
+// A block that a CTA began and that goes on in the CTAs after it.
 struct SplitRec {
-    uint32_t r, head, block;
+    Request q;
+    uint32_t head, block;
     uint32_t last;  // last CTA with a part; 0: none
 };
 
@@ -184,9 +202,11 @@ struct TensorArgs {
     uint32_t box_tokens;   // keys per copy
     uint32_t copies;       // copies per key tile and 64 channels
     uint32_t ctas;
-    SplitRec *rec;         // [ctas]
-    uint32_t *failed;      // [ctas]
     float *parts;          // [ctas][2][kPartFloats]: the part that continues a block, the part that begins one
+    SplitRec *rec;         // [ctas]
+    unsigned long long *timed_out;  // `call` once a wait of this call ran out
+    unsigned long long call;  // this call's tag, 48 bits
+    int32_t *status;       // [n_reqs]
     uint64_t wait_limit_ns;
     uint32_t debug_flags;
 };
@@ -221,6 +241,7 @@ __device__ __forceinline__ uint32_t block_count(const TensorArgs &p, const Reque
 struct Cursor {
     uint32_t r, head, block, off;  // off: tiles of the block done by earlier CTAs
     uint64_t left;                 // units still to do
+    bool whole;                    // units are blocks: none is split
     Request q;
 };
 struct Piece {
@@ -240,11 +261,11 @@ __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece
     w.block = c.block;
     w.q = c.q;
     w.t0 = lo + (int32_t)c.off;
-    const uint32_t n = (uint32_t)umin64((uint64_t)(hi - w.t0), c.left);
+    const uint32_t n = c.whole ? (uint32_t)(hi - lo) : (uint32_t)umin64((uint64_t)(hi - w.t0), c.left);
     w.t1 = w.t0 + (int32_t)n;
     w.starts = c.off == 0;
     w.ends = w.t1 == hi;
-    c.left -= n;
+    c.left -= c.whole ? 1 : n;
     c.off = 0;
     if (++c.block >= block_count<kM>(p, c.q)) {
         c.block = 0;
@@ -274,11 +295,16 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, uint32_t lane) {  // i
     return v;
 }
 
-// Units per KV head of request `r0 + lane` (0 past the end), by one warp:
-// requests of a few blocks are summed by their lane, larger ones by all.
+// Quotient of numbers that mostly fit 32 bits.
+__device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
+    return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
+}
+
+// Request r (none past the end) and its key tiles per KV head, a request per
+// lane of one warp: those of a few blocks are summed by their lane, larger
+// ones by all.  `most` grows to the tiles of the longest block.
 template <int kM>
-__device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane) {
-    Request q;
+__device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, Request &q, uint32_t &most) {
     q.q0 = q.n = q.kv = 0;
     q.status = SZ_OK;
     if (r < p.kv.n_reqs) q = load_request(p.kv, r);
@@ -289,6 +315,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane) {
         for (uint32_t b = 0; b < blocks; ++b) {
             block_tiles<kM>(p, q, b, &lo, &hi);
             units += (uint32_t)(hi - lo);
+            most = max(most, (uint32_t)(hi - lo));
         }
     uint32_t many = __ballot_sync(0xFFFFFFFFu, blocks > 4);
     while (many) {
@@ -303,6 +330,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane) {
         for (uint32_t b = lane; b < n; b += 32) {
             block_tiles<kM>(p, x, b, &lo, &hi);
             sum += (uint32_t)(hi - lo);
+            most = max(most, (uint32_t)(hi - lo));
         }
         sum = warp_sum(sum);
         if ((int)lane == src) units = sum;
@@ -311,11 +339,14 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane) {
 }
 
 struct PlanShared {
-    uint64_t warp_units[16];
+    uint64_t warp_units[16], warp_blocks[16];
+    uint32_t warp_most[16];
     uint64_t total;
-    uint64_t left;
-    uint32_t used;  // CTAs with work
+    uint64_t first, left;  // this CTA's units
+    uint32_t used;         // CTAs with work
     uint32_t r, head, block, off;
+    bool whole;
+    Request q;
 };
 
 // This CTA's share of the units, found by all of its threads.
@@ -323,54 +354,75 @@ template <int kM, int kThreads>
 __device__ void find_share(const TensorArgs &p, PlanShared &s) {
     constexpr uint32_t kW = kThreads / 32;
     const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const uint32_t rounds = (uint32_t)div_up(div_up(p.kv.n_reqs, 32), kW);
-    uint64_t mine = 0;
-    for (uint32_t i = 0; i < rounds; ++i)
-        mine += lane_units<kM>(p, (wid * rounds + i) * 32 + lane, lane);
-    mine = warp_sum(mine) * p.kv.heads;
-    if (lane == 0) s.warp_units[wid] = mine;
-    __syncthreads();
-    uint64_t total = 0, before = 0;
-    for (uint32_t w = 0; w < kW; ++w) {
-        if (w < wid) before += s.warp_units[w];
-        total += s.warp_units[w];
+    const uint32_t rounds = (p.kv.n_reqs + 32 * kW - 1) / (32 * kW);
+    uint64_t mine = 0, per_head = 0, blocks = 0;
+    uint32_t most = 0;
+    Request q;
+    for (uint32_t i = 0; i < rounds; ++i) {
+        per_head = lane_units<kM>(p, (wid * rounds + i) * 32 + lane, lane, q, most);
+        mine += per_head;
+        blocks += block_count<kM>(p, q);
     }
-    // every CTA that works has at least one unit, so that the parts of a block
-    // are those of consecutive CTAs
-    const uint32_t used = (uint32_t)umin64(p.ctas, umax64(1, total / kMinUnits));
+    mine = warp_sum(mine) * p.kv.heads;
+    blocks = warp_sum(blocks) * p.kv.heads;
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) {
+        s.warp_units[wid] = mine;
+        s.warp_blocks[wid] = blocks;
+        s.warp_most[wid] = most;
+    }
+    __syncthreads();
+    uint64_t total = 0, before = 0, total_blocks = 0, before_blocks = 0;
+    for (uint32_t w = 0; w < kW; ++w) {
+        if (w < wid) before += s.warp_units[w], before_blocks += s.warp_blocks[w];
+        total += s.warp_units[w];
+        total_blocks += s.warp_blocks[w];
+        most = max(most, s.warp_most[w]);
+    }
+    // A few short blocks: one CTA each, which costs less than joining parts.
+    const bool whole = total_blocks <= p.ctas && most <= kWholeTiles;
+    if (whole) total = total_blocks, before = before_blocks, mine = blocks;
+    // Every CTA that works has at least one unit, so that the parts of a block
+    // are those of consecutive CTAs.
+    const uint32_t used = (uint32_t)umin64(p.ctas, umax64(1, total));
     const bool works = blockIdx.x < used;
-    const uint64_t u0 = works ? blockIdx.x * total / used : 0, u1 = works ? (blockIdx.x + 1) * total / used : 0;
+    const uint64_t u0 = works ? divide(blockIdx.x * total, used) : 0, u1 = works ? divide((blockIdx.x + 1) * total, used) : 0;
     if (threadIdx.x == 0) {
         s.left = 0;
+        s.first = u0;
         s.total = total;
         s.used = used;
-        s.r = s.head = s.block = s.off = 0;
+        s.whole = whole;
     }
     __syncthreads();
     if (u1 > u0 && u0 >= before && u0 < before + mine) {  // one warp
         uint64_t rem = u0 - before;
         for (uint32_t i = 0; i < rounds; ++i) {
             const uint32_t r0 = (wid * rounds + i) * 32;
-            const uint64_t per_head = lane_units<kM>(p, r0 + lane, lane);
-            const uint64_t end = warp_scan(per_head * p.kv.heads, lane);
+            if (rounds > 1) per_head = lane_units<kM>(p, r0 + lane, lane, q, most);
+            const uint64_t units = whole ? block_count<kM>(p, q) : per_head;
+            const uint64_t end = warp_scan(units * p.kv.heads, lane);
             const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rem < end);
             if (hit == 0) {
                 rem -= __shfl_sync(0xFFFFFFFFu, end, 31);
                 continue;
             }
             const int src = __ffs(hit) - 1;
-            const uint64_t w = __shfl_sync(0xFFFFFFFFu, per_head, src);
-            rem -= __shfl_sync(0xFFFFFFFFu, end - per_head * p.kv.heads, src);
-            const uint32_t r = r0 + (uint32_t)src;
-            const uint32_t head = (uint32_t)(rem / w);
+            const uint64_t w = __shfl_sync(0xFFFFFFFFu, units, src);
+            rem -= __shfl_sync(0xFFFFFFFFu, end - units * p.kv.heads, src);
+            const uint32_t head = (uint32_t)divide(rem, w);
             rem -= head * w;
-            const Request q = load_request(p.kv, r);
-            for (uint32_t b0 = 0; b0 < block_count<kM>(p, q); b0 += 32) {
+            Request x;
+            x.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, src);
+            x.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+            x.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
+            x.status = SZ_OK;
+            for (uint32_t b0 = 0; b0 < block_count<kM>(p, x); b0 += 32) {
                 uint64_t n = 0;
-                if (b0 + lane < block_count<kM>(p, q)) {
+                if (b0 + lane < block_count<kM>(p, x)) {
                     int32_t lo, hi;
-                    block_tiles<kM>(p, q, b0 + lane, &lo, &hi);
-                    n = (uint32_t)(hi - lo);
+                    block_tiles<kM>(p, x, b0 + lane, &lo, &hi);
+                    n = whole ? 1u : (uint32_t)(hi - lo);
                 }
                 const uint64_t stop = warp_scan(n, lane);
                 const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < stop);
@@ -381,10 +433,11 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
                 const int at = __ffs(here) - 1;
                 rem -= __shfl_sync(0xFFFFFFFFu, stop - n, at);
                 if (lane == 0) {
-                    s.r = r;
+                    s.r = r0 + (uint32_t)src;
                     s.head = head;
                     s.block = b0 + (uint32_t)at;
                     s.off = (uint32_t)rem;
+                    s.q = x;
                     s.left = u1 - u0;
                 }
                 break;
@@ -393,6 +446,11 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
         }
     }
     __syncthreads();
+}
+
+// The CTA that has unit u.
+__device__ __forceinline__ uint32_t cta_of(const PlanShared &s, uint64_t u) {
+    return (uint32_t)divide((u + 1) * s.used - 1, s.total);
 }
 
 // Wait for a phase, by all lanes of a warp: false when the limit of device
@@ -435,7 +493,7 @@ __device__ __forceinline__ void hide(uint32_t (&s)[64], int32_t from, int32_t to
 
 struct Bars {
     uint64_t full[10], empty[10];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], pv_done[2];
     uint64_t drain;
 };
@@ -458,8 +516,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     // instructions want their operands
     const uint32_t tid = threadIdx.x, wid = same(tid >> 5), lane = tid & 31;
     const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t ring0 = smem0 + kM * S::kTileBytes;
-    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1;  // and the one after it
+    const uint32_t ring0 = smem0 + S::kQueries * S::kQueryBytes;
+    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1, kStatusWarp = kM * 4 + 3;
 
     if (wid == kMmaWarp) tmem_alloc(&tmem_base_s, S::kColumns);
     if (tid == 0) {
@@ -467,8 +525,10 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
-        mbar_init(&bars.q_full, 1);
-        mbar_init(&bars.q_empty, 1);
+        for (int i = 0; i < S::kQueries; ++i) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], 1);
+        }
         for (int x = 0; x < kM; ++x) {
             mbar_init(&bars.s_full[x], 1);
             mbar_init(&bars.p_full[x][0], 4);
@@ -504,12 +564,30 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     cur.block = plan.block;
     cur.off = plan.off;
     cur.left = plan.left;
-    if (cur.left > 0) cur.q = load_request(p.kv, cur.r);
+    cur.whole = plan.whole;
+    cur.q = plan.q;
     volatile uint32_t *const fail = &failed;
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
     if (wid >= kMmaWarp) {
-        if (wid >= kCopyWarp) {
+        give_registers<S::kFewRegs>();
+        if (wid == kStatusWarp) {
+        // ---------------------------------------------------------- statuses
+        for (uint32_t r = blockIdx.x; r < p.kv.n_reqs; r += gridDim.x) {
+            const Request q = load_request(p.kv, r);
+            sz_status st = q.status;
+            if (st == SZ_OK && q.n > 0 && q.kv > 0) {
+                int32_t begin, stop;
+                key_range(p, q, 0, q.n, &begin, &stop);
+                st = check_pages(p.kv, r, (uint32_t)begin / p.kv.page_tokens, (uint32_t)(q.kv - 1) / p.kv.page_tokens + 1);
+            }
+            if (lane == 0) {
+                p.status[r] = st;
+                __threadfence();  // a CTA that fails sets timed_out, then the statuses
+                if (*(volatile unsigned long long *)p.timed_out == p.call) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
+            }
+        }
+        } else if (wid >= kCopyWarp) {
         // ------------------------------------- copies: Q and K, or V
         const bool one = elect_one();
         const uint32_t is_v = wid - kCopyWarp;
@@ -520,16 +598,16 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         uint32_t use = is_v, pieces = 0;  // of the ring (K even, V odd), pieces begun
         bool ok = true;
         SplitRec rec;
-        rec.r = rec.head = rec.block = rec.last = 0;
-        uint64_t unit = blockIdx.x * plan.total / plan.used;
+        rec.last = 0;
+        uint64_t unit = plan.first;
         while (ok && next_piece<kM>(p, cur, w)) {
-            if (w.starts && !w.ends) {  // goes on in the CTAs up to the one that holds its last unit
+            if (w.starts && !w.ends) {
                 int32_t lo, hi;
                 block_tiles<kM>(p, w.q, w.block, &lo, &hi);
-                rec.r = w.r;
+                rec.q = w.q;
                 rec.head = w.head;
                 rec.block = w.block;
-                rec.last = (uint32_t)(((unit + (uint32_t)(hi - lo)) * plan.used - 1) / plan.total);
+                rec.last = cta_of(plan, unit + (uint32_t)(hi - lo) - 1);
             }
             unit += (uint32_t)(w.t1 - w.t0);
             const uint32_t first = w.block * kM * p.tile_tokens;
@@ -537,17 +615,18 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             const uint32_t tiles = kM == 1 || tokens <= p.tile_tokens ? 1u : 2u;
             const uint32_t head = same(w.head);
             if (!is_v) {
-                if (!(ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, fail, limit))) break;
+                const uint32_t buf = pieces % S::kQueries;
+                if (!(ok = warp_wait(&bars.q_empty[buf], (pieces / S::kQueries & 1) ^ 1, fail, limit))) break;
                 ++pieces;
                 if (one) {
                     const uint32_t rows = p.tile_tokens * p.group;
-                    mbar_arrive_expect_tx(&bars.q_full, tiles * rows * S::kHalves * kRowBytes);
+                    mbar_arrive_expect_tx(&bars.q_full[buf], tiles * rows * S::kHalves * kRowBytes);
                     if (!silent)
                         for (uint32_t x = 0; x < tiles; ++x)
 #pragma unroll
                             for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
-                                tma_load_3d(smem0 + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(head * p.group),
-                                            (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full));
+                                tma_load_3d(smem0 + buf * S::kQueryBytes + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(head * p.group),
+                                            (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full[buf]));
                 }
                 __syncwarp();
             }
@@ -584,12 +663,13 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 if (t + 1 < t_end) page = page_at(t + 1);
             }
         }
-        if (is_v && lane == 0) p.rec[blockIdx.x] = rec;
+        if (p.rec && is_v && lane == 0) p.rec[blockIdx.x] = rec;
         if (!ok && !silent) {  // copies still under way must land before the CTA ends
             // (this warp's uses of the last round of slots)
             for (uint32_t u = use > 2 * S::kSlots ? use - 2 * S::kSlots : is_v; u < use; u += 2)
                 mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
-            if (pieces) mbar_wait(&bars.q_full, (pieces - 1) & 1, limit);
+            for (uint32_t u = pieces > S::kQueries ? pieces - S::kQueries : 0; u < pieces; ++u)
+                mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, limit);
         }
         } else if (wid == kMmaWarp) {
         // ---------------------------------------------------------- products
@@ -607,8 +687,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             m = same((kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens) ? 1u : 2u);
             return same(have ? 1u : 0u) != 0;
         };
-        auto score = [&](uint32_t m, uint32_t at) {  // S_m = Q_m K^T
-            const uint32_t a = q_lo + m * (S::kTileBytes >> 4), b = k_lo + at * (S::kTileBytes >> 4);
+        auto score = [&](uint32_t m, uint32_t at, uint32_t buf) {  // S_m = Q_m K^T
+            const uint32_t a = q_lo + buf * (S::kQueryBytes >> 4) + m * (S::kTileBytes >> 4), b = k_lo + at * (S::kTileBytes >> 4);
             if (one) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -622,31 +702,34 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         };
         bool have = take(t, t_end, kv, tiles);
         bool first = true;  // the piece's first tile
-        uint32_t pieces = 0, slot = 1 % S::kSlots, phase = 0;  // of the ring, at this tile's V
+        uint32_t pieces = 0;                         // index of the piece at hand
+        uint32_t slot = 1 % S::kSlots, phase = 0;  // of the ring, at this tile's V
         if (have) {
-            wait_or_fail(&bars.q_full, 0, fail, limit);
+            wait_or_fail(&bars.q_full[0], 0, fail, limit);
             wait_or_fail(&bars.full[0], 0, fail, limit);
-            ++pieces;
             tc_fence_after();
 #pragma unroll
             for (uint32_t m = 0; m < kM; ++m)
-                if (m < tiles) score(m, 0);
+                if (m < tiles) score(m, 0, 0);
             if (one) {
                 mma_commit(&bars.empty[0]);
-                if (t + 1 == t_end) mma_commit(&bars.q_empty);
+                if (t + 1 == t_end) mma_commit(&bars.q_empty[0]);
             }
         }
-        while (have && *fail == 0) {
+        while (have && same(*fail) == 0) {
             int32_t nt = t + 1, nt_end = t_end, nkv = kv;
             uint32_t ntiles = tiles;
             bool more = true, nfirst = false;
             if (nt >= t_end) {
                 more = take(nt, nt_end, nkv, ntiles);
                 nfirst = true;
+                ++pieces;
                 if (!more) ntiles = 0;
             }
-            // V of this tile and K of the next (and the next piece's Q) first, so
-            // that nothing is waited for between the weights and the products
+            const uint32_t buf = pieces % S::kQueries;
+            // V of this tile and K of the next first, so that nothing is waited
+            // for between the weights and the products; but a next piece's Q and
+            // K may be some way off, and this piece's last products go ahead
             const uint32_t v_slot = slot, k_slot = slot + 1 == S::kSlots ? 0 : slot + 1;
             const uint32_t v_phase = phase, k_phase = phase ^ (k_slot == 0 ? 1u : 0u);
             slot = k_slot + 1 == S::kSlots ? 0 : k_slot + 1;
@@ -667,13 +750,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             }
-            if (more) {
-                if (nfirst) {
-                    wait_or_fail(&bars.q_full, pieces & 1, fail, limit);
-                    ++pieces;
-                }
-                wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
-            }
+            if (more && !nfirst) wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
             const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
 #pragma unroll
             for (uint32_t m = 0; m < kM; ++m) {
@@ -694,13 +771,21 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         __syncwarp();
                     }
                 }
-                if (m < ntiles) score(m, k_slot);
+                if (m < ntiles && !nfirst) score(m, k_slot, buf);
+            }
+            if (more && nfirst) {
+                wait_or_fail(&bars.q_full[buf], pieces / S::kQueries & 1, fail, limit);
+                wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t m = 0; m < kM; ++m)
+                    if (m < ntiles) score(m, k_slot, buf);
             }
             if (one) {
                 mma_commit(&bars.empty[v_slot]);
                 if (more) {
                     mma_commit(&bars.empty[k_slot]);
-                    if (nt + 1 == nt_end) mma_commit(&bars.q_empty);
+                    if (nt + 1 == nt_end) mma_commit(&bars.q_empty[buf]);
                 }
             }
             t = nt;
@@ -720,6 +805,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         }
     } else {
         // ----------------------------------------------------------- softmax
+        take_registers<S::kManyRegs>();
 
         const uint32_t m_tile = wid / 4;
         const uint32_t row = tid & 127;
@@ -823,11 +909,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             const float2 both = unpack2(sum);
             const float l = both.x + both.y;
             tc_fence_after();
-            if (!warp_live) continue;
             const bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
             const float ref = m * p.c;  // log2 units
             if (w.starts && w.ends) {
+                if (!warp_live) continue;
                 const bool any = begin < stop;
                 const float inv = any ? 1.0f / l : 0.0f;
                 uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
@@ -848,99 +934,133 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                     p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any ? (l > 0.0f || l != l ? (ref + log2f(l)) * kLn2 : -INFINITY) : -INFINITY;
             } else {
                 float *part = p.parts + (size_t)(blockIdx.x * 2 + (w.starts ? 1 : 0)) * S::kPartFloats;
-                const uint32_t at = m_tile * kTileRows + row;
+                if (warp_live) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + i * 32, o);
-                    tmem_wait_ld();
-                    if (mine)
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + i * 32, o);
+                        tmem_wait_ld();
+                        if (mine)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *(uint4 *)(part + (size_t)at * D + i * 32 + j * 4) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            for (int j = 0; j < 8; ++j)
+                                *(uint4 *)(part + S::part_o(m_tile, i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                    if (mine) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
                 }
-                if (mine) *(float2 *)(part + kM * kTileRows * D + at * 2) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
             }
         }
         tc_fence_before();
     }
     // ------------------------------------------------------------------ end
     __syncthreads();
-    if (tid == 0) p.failed[blockIdx.x] = failed;
+    if (failed) {  // rows may be unfinished: no result of this call stands
+        if (tid == 0) {
+            atomicExch(p.timed_out, p.call);
+            __threadfence();
+        }
+        __syncthreads();
+        for (uint32_t r = tid; r < p.kv.n_reqs; r += S::kThreads) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
+    }
     if (wid == kMmaWarp) tmem_free(tmem, S::kColumns);
 }
 
-// Statuses of all requests, then the blocks whose keys were split: a warp per
-// row joins its parts in order.
-constexpr int kJoinThreads = 256;
-constexpr uint32_t kJoinY = 4;
+// Join the parts of split blocks.  Two parts join like two sets of keys:
+// (m, l, o) and (m', l', o') to M = max, l 2^(m - M) + l' 2^(m' - M), the
+// same for o.  What bounds it is the latency of its few loads, so it is spread
+// out: a block of threads per CTA that began a split block, row tile and
+// D/8 channels; a thread holds one row's and, where rows are few (a decode
+// step, whose parts are many), one slice of the parts.  Slices and parts are
+// added in a fixed order.
+constexpr int kJoinThreads = 128;
+constexpr uint32_t kJoinGroups = 8;
 
 template <typename T, int D, int kM>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ TensorArgs p, int32_t *status) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __grid_constant__ TensorArgs p) {
     using S = Shape<D, kM>;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    // lengths and tables were there before the attention kernel began
-    const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x, blocks = gridDim.x * gridDim.y;
-    for (uint32_t r = block; r < p.kv.n_reqs; r += blocks) {
-        const Request q = load_request(p.kv, r);
-        bool bad = false;
-        if (q.status == SZ_OK && q.n > 0 && q.kv > 0) {
-            int32_t begin, stop;
-            key_range(p, q, 0, q.n, &begin, &stop);
-            for (uint32_t i = (uint32_t)begin / p.kv.page_tokens + tid; i < (uint32_t)(q.kv - 1) / p.kv.page_tokens + 1; i += kJoinThreads)
-                bad |= page_of(p.kv, r, i) < 0;
-        }
-        bad = __syncthreads_or(bad) != 0;
-        if (tid == 0) status[r] = q.status != SZ_OK ? q.status : bad ? SZ_ERR_INVALID : SZ_OK;
-    }
+    constexpr int kChunks = D / 4 / (int)kJoinGroups, kBatch = 4;
+    __shared__ float shared[kJoinThreads][kChunks * 4 + 3];
+    const uint32_t tid = threadIdx.x, c0 = blockIdx.x, chunk = blockIdx.y * kChunks, m_tile = blockIdx.z;
     grid_dependency_wait();
-    uint32_t late = 0;
-    for (uint32_t c = tid; c < p.ctas; c += kJoinThreads) late |= p.failed[c];
-    if (__syncthreads_or(late != 0)) {  // some rows were never finished
-        if (tid == 0)
-            for (uint32_t r = block; r < p.kv.n_reqs; r += blocks)
-                if (status[r] == SZ_OK) status[r] = SZ_ERR_DEVICE_TIMEOUT;
-        return;
-    }
-    const uint32_t c0 = blockIdx.x;
-    const SplitRec rec = p.rec[c0];
-    if (rec.last == 0) return;
-    const Request q = load_request(p.kv, rec.r);
-    const uint32_t first = rec.block * kM * p.tile_tokens;
-    const uint32_t tokens = umin32((uint32_t)q.n - first, kM * p.tile_tokens);
-    const uint32_t parts = rec.last - c0 + 1;
-    for (uint32_t i = blockIdx.y * (kJoinThreads / 32) + wid; i < tokens * p.group; i += kJoinY * (kJoinThreads / 32)) {
-        const uint32_t tok = i / p.group, g = i % p.group;
-        const uint32_t at = tok / p.tile_tokens * kTileRows + (tok % p.tile_tokens) * p.group + g;
-        auto part_of = [&](uint32_t k) { return p.parts + (size_t)(k == 0 ? c0 * 2 + 1 : (c0 + k) * 2) * S::kPartFloats; };
-        float top = -INFINITY;
-        for (uint32_t k = lane; k < parts; k += 32) top = fmaxf(top, part_of(k)[kM * kTileRows * D + at * 2]);
+    const SplitRec w = p.rec[c0];
+    if (w.last == 0) return;
+    const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
+    if ((uint32_t)w.q.n <= first) return;
+    const uint32_t rows = umin32((uint32_t)w.q.n - first, p.tile_tokens) * p.group, parts = w.last - c0 + 1;
+    const uint32_t row_span = rows <= 1 ? 1u : 1u << (32 - __clz(rows - 1)), slices = kJoinThreads / row_span;
+    const uint32_t row = tid % row_span, slice = tid / row_span;
+    const float *const base = p.parts + (size_t)(c0 * 2) * S::kPartFloats;  // part 0 is the first CTA's second slot
+    float top = -INFINITY, sum = 0.0f, o[kChunks][4] = {};
+    for (uint32_t k0 = slice; k0 < parts && row < rows; k0 += kBatch * slices) {
+        float4 v[kBatch][kChunks];
+        float2 ml[kBatch];
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        float sum = 0.0f, o[D / 32] = {};
-#pragma unroll 4
-        for (uint32_t k = 0; k < parts; ++k) {
-            const float *part = part_of(k);
-            const float2 ml = *(const float2 *)(part + kM * kTileRows * D + at * 2);
-            if (ml.y == 0.0f) continue;  // nothing visible there
-            const float f = exp2f(ml.x - top);
-            sum += ml.y * f;
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t k = umin32(k0 + i * slices, parts - 1);
+            const float *from = base + (size_t)(k == 0 ? 1 : 2 * k) * S::kPartFloats;
+            ml[i] = __ldcg((const float2 *)(from + S::part_ml(m_tile, row)));
+            if (k0 + i * slices >= parts) ml[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) o[e] += part[(size_t)at * D + lane * (D / 32) + e] * f;
+            for (int j = 0; j < kChunks; ++j) v[i][j] = __ldcg((const float4 *)(from + S::part_o(m_tile, chunk + j, row)));
         }
-        int32_t begin, stop;
-        key_range(p, q, (int32_t)(first + tok), (int32_t)(first + tok) + 1, &begin, &stop);
-        const bool any = begin < stop;
-        const float inv = any ? 1.0f / sum : 0.0f;
-        const uint32_t token = (uint32_t)q.q0 + first + tok, head = rec.head * p.group + g;
-        uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
+        float high = top;
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e)
-            *(uint32_t *)(out + lane * (D / 32) + 2 * e) =
-                any ? Half2<T>::narrow(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-        if (lane == 0 && p.a.d_lse_or_null)
-            p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any && sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        for (int i = 0; i < kBatch; ++i) high = fmaxf(high, ml[i].x);
+        const float keep = high == top ? 1.0f : exp2f(top - high);
+        top = high;
+        sum *= keep;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] *= keep;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (ml[i].y == 0.0f) continue;  // nothing visible there
+            const float f = exp2f(ml[i].x - top);
+            sum += ml[i].y * f;
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) {
+                o[j][0] += v[i][j].x * f;
+                o[j][1] += v[i][j].y * f;
+                o[j][2] += v[i][j].z * f;
+                o[j][3] += v[i][j].w * f;
+            }
+        }
     }
+    if (slices > 1) {
+        float *const mine = shared[tid];
+#pragma unroll
+        for (int j = 0; j < kChunks * 4; ++j) mine[j] = o[j / 4][j % 4];
+        mine[kChunks * 4] = top;
+        mine[kChunks * 4 + 1] = sum;
+        __syncthreads();
+        if (slice == 0)
+            for (uint32_t k = 1; k < slices && k < parts; ++k) {
+                const float *const from = shared[k * row_span + row];
+                const float high = fmaxf(top, from[kChunks * 4]);
+                if (from[kChunks * 4 + 1] == 0.0f) continue;
+                const float keep = high == top ? 1.0f : exp2f(top - high), f = exp2f(from[kChunks * 4] - high);
+                top = high;
+                sum = sum * keep + from[kChunks * 4 + 1] * f;
+#pragma unroll
+                for (int j = 0; j < kChunks * 4; ++j) o[j / 4][j % 4] = o[j / 4][j % 4] * keep + from[j] * f;
+            }
+    }
+    if (slice != 0 || row >= rows) return;
+    const uint32_t tok = row / p.group;
+    int32_t begin, stop;
+    key_range(p, w.q, (int32_t)(first + tok), (int32_t)(first + tok) + 1, &begin, &stop);
+    const bool any = begin < stop;
+    const float inv = any ? 1.0f / sum : 0.0f;
+    const uint32_t token = (uint32_t)w.q.q0 + first + tok, head = w.head * p.group + row % p.group;
+    uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1] + chunk * 4;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        uint2 x = make_uint2(0u, 0u);
+        if (any) x = make_uint2(Half2<T>::narrow(o[j][0] * inv, o[j][1] * inv), Half2<T>::narrow(o[j][2] * inv, o[j][3] * inv));
+        ((uint2 *)out)[j] = x;
+    }
+    if (chunk == 0 && p.a.d_lse_or_null)
+        p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any && sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------- host side
@@ -991,7 +1111,18 @@ static bool tensor_shape(const sz_paged_kv &kv, const sz_attention_args &a) {
 template <int D, int kM>
 static uint64_t tensor_workspace() {
     const uint64_t ctas = (uint64_t)kMaxTensorSms * Shape<D, kM>::kCtasPerSm;
-    return ctas * (sizeof(SplitRec) + 16 + 2 * 4ull * Shape<D, kM>::kPartFloats);
+    return 8 + ctas * sizeof(SplitRec) + 2 * 4ull * Shape<D, kM>::kPartFloats * ctas;
+}
+
+// A tag for a call's words in the workspace: 48 bits, from a random start, so
+// that words of earlier calls, or of other memory, do not carry it.
+static unsigned long long next_call() {
+    static std::atomic<unsigned long long> next{[] {
+        std::random_device r;
+        return ((unsigned long long)r() << 32 | r()) ^ (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count();
+    }()};
+    for (;;)
+        if (const unsigned long long tag = next.fetch_add(1) & 0xFFFFFFFFFFFFull) return tag;
 }
 
 uint64_t attention_workspace(uint32_t head_dim) {
@@ -1018,9 +1149,14 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.parts = reinterpret_cast<float *>(at);
     at += (size_t)p.ctas * 2 * 4 * S::kPartFloats;
-    p.rec = reinterpret_cast<SplitRec *>(at);
-    at += (size_t)p.ctas * sizeof(SplitRec);
-    p.failed = reinterpret_cast<uint32_t *>(at);
+    p.timed_out = reinterpret_cast<unsigned long long *>(at);
+    // Where the sizes known here already say that no block will be split
+    // (find_share comes to the same), nothing needs joining.
+    const uint64_t span = (uint64_t)S::kTiles * p.tile_tokens, blocks = kv.heads * (kv.n_reqs + kv.n_tokens / span);
+    const bool split = blocks > p.ctas || div_up((uint64_t)kv.max_pages * kv.page_tokens, p.key_tile) > kWholeTiles;
+    p.rec = split ? reinterpret_cast<SplitRec *>(at + 8) : nullptr;
+    p.call = next_call();
+    p.status = status;
     p.wait_limit_ns = wait_limit_ns();
     p.debug_flags = debug_flags();
     CUtensorMap q_map, k_map, v_map;
@@ -1036,7 +1172,8 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     if (const cudaError_t e = allow_shared<attention_kernel<T, D, kM>>(S::kSmem)) return e;
     attention_kernel<T, D, kM><<<p.ctas, S::kThreads, S::kSmem, s>>>(p, q_map, k_map, v_map);
     if (const cudaError_t e = cudaGetLastError()) return e;
-    return launch_after(attention_join_kernel<T, D, kM>, dim3(p.ctas, kJoinY), dim3(kJoinThreads), 0, s, p, status);
+    if (!split) return cudaSuccess;
+    return launch_after(attention_join_kernel<T, D, kM>, dim3(p.ctas, kJoinGroups, kM), dim3(kJoinThreads), 0, s, p);
 }
 
 template <typename T>
