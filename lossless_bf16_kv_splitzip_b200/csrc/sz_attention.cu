@@ -151,6 +151,9 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
+#ifndef SZ_BU
+#define SZ_BU (kM == 1 ? 1 : 2)
+#endif
 #ifndef SZ_POLY
 #define SZ_POLY 4
 #endif
@@ -166,9 +169,6 @@ struct Shape {
     static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 4);
     static constexpr int kSoftmaxThreads = kM * 128;
     static constexpr int kThreads = kSoftmaxThreads + 128;
-    // Registers a thread, traded between warpgroups: launched with 168 (three
-    // of them) or 128 (two, twice per SM); 2 * 208 + 88 = 3 * 168, 168 + 88 = 2 * 128.
-    static constexpr int kManyRegs = kM == 2 ? 208 : 168, kFewRegs = 88;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
     static constexpr uint32_t kQueryBytes = kM * kTileBytes;
@@ -237,6 +237,11 @@ __device__ __forceinline__ uint32_t block_count(const TensorArgs &p, const Reque
     return ((uint32_t)q.n + span - 1) / span;
 }
 
+// What a block costs beside its tiles (queries, first scores, output), in
+// tiles: the units of a block begin with as many that hold no tile.
+template <int kM>
+constexpr uint32_t kBlockUnits = SZ_BU;
+
 // Where a CTA stands in the order of units.
 struct Cursor {
     uint32_t r, head, block, off;  // off: tiles of the block done by earlier CTAs
@@ -253,6 +258,7 @@ struct Piece {
 
 template <int kM>
 __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece &w) {
+    do {
     if (c.left == 0) return false;
     int32_t lo, hi;
     block_tiles<kM>(p, c.q, c.block, &lo, &hi);
@@ -260,12 +266,18 @@ __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece
     w.head = c.head;
     w.block = c.block;
     w.q = c.q;
-    w.t0 = lo + (int32_t)c.off;
-    const uint32_t n = c.whole ? (uint32_t)(hi - lo) : (uint32_t)umin64((uint64_t)(hi - w.t0), c.left);
-    w.t1 = w.t0 + (int32_t)n;
-    w.starts = c.off == 0;
+    if (c.whole) {
+        w.t0 = lo;
+        w.t1 = hi;
+        c.left -= 1;
+    } else {
+        const uint32_t end = c.off + (uint32_t)umin64((uint32_t)(hi - lo) + kBlockUnits<kM> - c.off, c.left);
+        w.t0 = lo + max((int32_t)(c.off - kBlockUnits<kM>), 0);
+        w.t1 = lo + max((int32_t)(end - kBlockUnits<kM>), 0);
+        c.left -= end - c.off;
+    }
+    w.starts = w.t0 == lo;
     w.ends = w.t1 == hi;
-    c.left -= c.whole ? 1 : n;
     c.off = 0;
     if (++c.block >= block_count<kM>(p, c.q)) {
         c.block = 0;
@@ -278,6 +290,7 @@ __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece
             if (c.r >= p.kv.n_reqs) c.left = 0;
         }
     }
+    } while (w.t0 == w.t1);  // a share may end in a block's first units, before its first tile
     return true;
 }
 
@@ -314,7 +327,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
     if (blocks <= 4)
         for (uint32_t b = 0; b < blocks; ++b) {
             block_tiles<kM>(p, q, b, &lo, &hi);
-            units += (uint32_t)(hi - lo);
+            units += (uint32_t)(hi - lo) + kBlockUnits<kM>;
             most = max(most, (uint32_t)(hi - lo));
         }
     uint32_t many = __ballot_sync(0xFFFFFFFFu, blocks > 4);
@@ -329,7 +342,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
         uint64_t sum = 0;
         for (uint32_t b = lane; b < n; b += 32) {
             block_tiles<kM>(p, x, b, &lo, &hi);
-            sum += (uint32_t)(hi - lo);
+            sum += (uint32_t)(hi - lo) + kBlockUnits<kM>;
             most = max(most, (uint32_t)(hi - lo));
         }
         sum = warp_sum(sum);
@@ -422,7 +435,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
                 if (b0 + lane < block_count<kM>(p, x)) {
                     int32_t lo, hi;
                     block_tiles<kM>(p, x, b0 + lane, &lo, &hi);
-                    n = whole ? 1u : (uint32_t)(hi - lo);
+                    n = whole ? 1u : (uint32_t)(hi - lo) + kBlockUnits<kM>;
                 }
                 const uint64_t stop = warp_scan(n, lane);
                 const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < stop);
@@ -570,7 +583,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
     if (wid >= kMmaWarp) {
-        give_registers<S::kFewRegs>();
         if (wid == kStatusWarp) {
         // ---------------------------------------------------------- statuses
         for (uint32_t r = blockIdx.x; r < p.kv.n_reqs; r += gridDim.x) {
@@ -599,7 +611,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         bool ok = true;
         SplitRec rec;
         rec.last = 0;
-        uint64_t unit = plan.first;
         while (ok && next_piece<kM>(p, cur, w)) {
             if (w.starts && !w.ends) {
                 int32_t lo, hi;
@@ -607,9 +618,9 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 rec.q = w.q;
                 rec.head = w.head;
                 rec.block = w.block;
-                rec.last = cta_of(plan, unit + (uint32_t)(hi - lo) - 1);
+                // of the units left, those of this block's other tiles come last
+                rec.last = cta_of(plan, plan.first + plan.left + (uint32_t)(hi - w.t1) - 1);
             }
-            unit += (uint32_t)(w.t1 - w.t0);
             const uint32_t first = w.block * kM * p.tile_tokens;
             const uint32_t tokens = umin32((uint32_t)w.q.n - first, kM * p.tile_tokens);
             const uint32_t tiles = kM == 1 || tokens <= p.tile_tokens ? 1u : 2u;
@@ -805,7 +816,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         }
     } else {
         // ----------------------------------------------------------- softmax
-        take_registers<S::kManyRegs>();
 
         const uint32_t m_tile = wid / 4;
         const uint32_t row = tid & 127;

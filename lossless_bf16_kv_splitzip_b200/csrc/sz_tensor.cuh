@@ -114,18 +114,7 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// --------------------------------------------------- registers and arithmetic
-// Warpgroups of 4 warps trade registers; the shares add up to what the block
-// was launched with.
-template <int kCount>
-__device__ __forceinline__ void take_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
-}
-template <int kCount>
-__device__ __forceinline__ void give_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
-}
-
+// -------------------------------------------------------------- arithmetic
 // Two 32-bit numbers in one instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;

@@ -19,6 +19,7 @@ status tensor with one word per request.  Neither has a gradient.
 """
 from __future__ import annotations
 
+import functools
 import math
 import struct
 
@@ -26,43 +27,56 @@ _KV = struct.Struct("<9Q4I4Q2IQ")  # sz_paged_kv
 _APPEND = struct.Struct("<18Q4I2f")  # sz_append_args
 _ATTENTION = struct.Struct("<7Q3If")  # sz_attention_args
 
+# What every call needs, set by the first one.  A decode step makes these
+# calls per layer, so their host side is kept to a few microseconds: one
+# packed struct instead of a ctypes structure's fields, device ordinals
+# instead of device objects.
+_T = None        # torch
 _TYPES: dict = {}
+_LIB = None
+_STREAM = None   # device ordinal -> raw handle of its current stream
 
 
-def _torch():
+def _load():
+    global _T, _LIB, _STREAM
     import torch
-    if not _TYPES:
-        _TYPES[torch.bfloat16] = 1
-        _TYPES[torch.float16] = 2
+
+    from . import lib
+    _LIB = lib()
+    _TYPES[torch.bfloat16] = 1
+    _TYPES[torch.float16] = 2
+    _STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _T = torch
     return torch
 
 
 def _ints(name, t, ndim, torch):
-    if t.dtype != torch.int32 or t.dim() != ndim or t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dtype is not torch.int32 or t.dim() != ndim or t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("%s must be an int32 tensor of %d dimension(s) with entries side by side" % (name, ndim))
-    return t
 
 
 def _rows(name, t, dtype, tokens, dim):
-    if t.dtype != dtype or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim:
-        raise ValueError("%s must be %s [%d tokens, heads, %d], got %s %s" % (name, dtype, tokens, dim, t.dtype, tuple(t.shape)))
+    """Heads of rows [tokens, heads, dim] and their strides."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+        raise ValueError("%s must be %s [%d tokens, heads, %d], got %s %s" % (name, dtype, tokens, dim, t.dtype, tuple(shape)))
     s = t.stride()
     if s[2] != 1:
         raise ValueError("%s needs its channels side by side" % name)
     if t.requires_grad:
         raise ValueError("%s requires a gradient, and this operator has none" % name)
-    return s
+    return shape[1], s[0], s[1]
 
 
-def _pack_kv(torch, k_pages, v_pages, page_table, q_begin, kv_len, tokens):
+def _pack_kv(torch, k_pages, v_pages, shape, page_table, q_begin, kv_len, tokens):
     code = _TYPES.get(k_pages.dtype)
-    if code is None or v_pages.dtype != k_pages.dtype:
+    if code is None or v_pages.dtype is not k_pages.dtype:
         raise TypeError("pages are bfloat16 or float16, the same for keys and values; got %s and %s" % (k_pages.dtype, v_pages.dtype))
-    shape = k_pages.shape
     if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("pages are two tensors [pages, heads, page tokens, channels] of one shape")
-    ks, vs = k_pages.stride(), v_pages.stride()
-    if ks[3] != 1 or vs[3] != 1:
+    k0, k1, k2, k3 = k_pages.stride()
+    v0, v1, v2, v3 = v_pages.stride()
+    if k3 != 1 or v3 != 1:
         raise ValueError("pages need their channels side by side")
     _ints("page_table", page_table, 2, torch)
     _ints("q_begin", q_begin, 1, torch)
@@ -70,43 +84,34 @@ def _pack_kv(torch, k_pages, v_pages, page_table, q_begin, kv_len, tokens):
     reqs, max_pages = page_table.shape
     if q_begin.shape[0] != reqs + 1 or kv_len.shape[0] != reqs:
         raise ValueError("%d requests in page_table, %d in q_begin, %d in kv_len" % (reqs, q_begin.shape[0] - 1, kv_len.shape[0]))
-    return _KV.pack(k_pages.data_ptr(), v_pages.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], shape[0], shape[1], shape[3],
-                    shape[2], code, page_table.data_ptr(), page_table.stride(0) if reqs > 1 else max_pages, q_begin.data_ptr(),
-                    kv_len.data_ptr(), reqs, max_pages, tokens)
+    return _KV.pack(k_pages.data_ptr(), v_pages.data_ptr(), k0, k1, k2, v0, v1, v2, shape[0], shape[1], shape[3], shape[2], code,
+                    page_table.data_ptr(), page_table.stride(0) if reqs > 1 else max_pages, q_begin.data_ptr(), kv_len.data_ptr(), reqs,
+                    max_pages, tokens)
 
 
-class _On:
-    """The device and stream of one call: the tensors' device made current,
-    and the given stream, if any."""
+def _device(tensors):
+    """The one CUDA device of all tensors (None among them skipped)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on %s and %s" % (tensors[0].device, t.device))
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device, not on %s" % tensors[0].device)
+    return dev
 
-    def __init__(self, torch, tensors, stream):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError("tensors on %s and %s" % (dev, t.device))
-        if dev.type != "cuda":
-            raise ValueError("the tensors must be on a CUDA device, not on %s" % dev)
-        self.guards = []
-        if torch.cuda.current_device() != dev.index:
-            self.guards.append(torch.cuda.device(dev))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
-            if stream.device != dev:
-                raise ValueError("a stream of %s for tensors on %s" % (stream.device, dev))
-            self.guards.append(torch.cuda.stream(stream))
-        self.stream = stream
-        self.dev = dev
-        self.torch = torch
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.dev, (self.stream or self.torch.cuda.current_stream(self.dev)).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _elsewhere(call, dev, stream):
+    """``call`` with another device or stream made current, or None where the
+    current ones serve already."""
+    torch = _T
+    if stream is None and torch.cuda.current_device() == dev:
+        return None
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("a stream of %s for tensors on cuda:%d" % (stream.device, dev))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call()
 
 
 def append_kv(k, v, k_pages, v_pages, page_table, q_begin, kv_len, *, q=None, q_out=None, rope_freqs=None,
@@ -127,30 +132,30 @@ def append_kv(k, v, k_pages, v_pages, page_table, q_begin, kv_len, *, q=None, q_
     (rows r and requests + r without ``hist_rows``).
 
     Returns (q_out or None, status int32 [requests])."""
-    torch = _torch()
-    tokens, dim, dtype = k.shape[0], k_pages.shape[-1], k_pages.dtype
-    kv = _pack_kv(torch, k_pages, v_pages, page_table, q_begin, kv_len, tokens)
-    ks, vs = _rows("k", k, dtype, tokens, dim), _rows("v", v, dtype, tokens, dim)
-    if k.shape[1] != k_pages.shape[1] or v.shape[1] != k_pages.shape[1]:
-        raise ValueError("pages of %d heads, k of %d, v of %d" % (k_pages.shape[1], k.shape[1], v.shape[1]))
-    qs, q_heads = (0, 0, 0), 0
+    torch = _T or _load()
+    shape, dtype = k_pages.shape, k_pages.dtype
+    tokens, dim = k.shape[0], shape[-1]
+    kv = _pack_kv(torch, k_pages, v_pages, shape, page_table, q_begin, kv_len, tokens)
+    hk, k0, k1 = _rows("k", k, dtype, tokens, dim)
+    hv, v0, v1 = _rows("v", v, dtype, tokens, dim)
+    if hk != shape[1] or hv != shape[1]:
+        raise ValueError("pages of %d heads, k of %d, v of %d" % (shape[1], hk, hv))
+    q_heads = q0 = q1 = rot_dim = n_hists = 0
     if q is not None:
-        qs, q_heads = _rows("q", q, dtype, tokens, dim), q.shape[1]
+        q_heads, q0, q1 = _rows("q", q, dtype, tokens, dim)
         if q_out is not None and q_out.shape != q.shape:
             raise ValueError("q_out of shape %s for q of %s" % (tuple(q_out.shape), tuple(q.shape)))
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm need q")
-    rot_dim = 0
     if rope_freqs is not None:
-        if rope_freqs.dtype != torch.float64 or rope_freqs.dim() != 1 or not rope_freqs.is_contiguous():
+        if rope_freqs.dtype is not torch.float64 or rope_freqs.dim() != 1 or not rope_freqs.is_contiguous():
             raise ValueError("rope_freqs must be a contiguous float64 vector")
         rot_dim = 2 * rope_freqs.shape[0]
-    if positions is not None and (positions.dtype != torch.int64 or positions.shape != (tokens,) or not positions.is_contiguous()):
+    if positions is not None and (positions.dtype is not torch.int64 or positions.shape != (tokens,) or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int64 tensor [%d]" % tokens)
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype != dtype or w.shape != (dim,) or not w.is_contiguous()):
+        if w is not None and (w.dtype is not dtype or w.shape != (dim,) or not w.is_contiguous()):
             raise ValueError("%s must be a contiguous %s tensor [%d]" % (name, dtype, dim))
-    n_hists = 0
     if hists is not None:
         if hists.dtype not in (torch.int32, torch.uint32) or hists.shape[-1] != 256 or not hists.is_contiguous():
             raise ValueError("hists must be a contiguous 32-bit tensor of rows of 256 counts")
@@ -160,24 +165,33 @@ def append_kv(k, v, k_pages, v_pages, page_table, q_begin, kv_len, *, q=None, q_
             raise ValueError("hist_rows needs hists")
         if hist_rows.dtype not in (torch.int32, torch.uint32) or hist_rows.numel() != 2 * kv_len.shape[0] or not hist_rows.is_contiguous():
             raise ValueError("hist_rows must be a contiguous 32-bit tensor of %d rows" % (2 * kv_len.shape[0]))
-    from . import _check, lib
-    with _On(torch, (k_pages, v_pages, k, v, page_table, q_begin, kv_len, q, q_out, rope_freqs, positions, q_norm, k_norm, hists,
-                     hist_rows), stream) as (dev, s):
-        status = torch.empty(kv_len.shape[0], dtype=torch.int32, device=dev)
-        qos = (0, 0, 0)
+    dev = _device((k_pages, v_pages, k, v, page_table, q_begin, kv_len, q, q_out, rope_freqs, positions, q_norm, k_norm, hists, hist_rows))
+
+    def call():
+        status = torch.empty_like(kv_len)
+        out, o0, o1 = q_out, 0, 0
         if q is not None:
-            if q_out is None:
-                q_out = torch.empty((tokens, q_heads, dim), dtype=dtype, device=dev)
-            qos = _rows("q_out", q_out, dtype, tokens, dim)
+            if out is None:
+                out = torch.empty_like(q)
+            _, o0, o1 = _rows("q_out", out, dtype, tokens, dim)
+        args = _APPEND.pack(k.data_ptr(), v.data_ptr(), k0, k1, v0, v1, _at(q), _at(out), q0, q1, o0, o1, _at(q_norm), _at(k_norm),
+                            _at(rope_freqs), _at(positions), _at(hists), _at(hist_rows), q_heads, rot_dim, 1 if rope_interleaved else 0,
+                            n_hists, rope_scale, eps)
+        st = _LIB.sz_append_kv(kv, args, status.data_ptr(), _STREAM(dev))
+        if st:
+            _fail(st, "sz_append_kv")
+        return out, status
 
-        def at(t):
-            return 0 if t is None else t.data_ptr()
+    return _elsewhere(call, dev, stream) or call()
 
-        args = _APPEND.pack(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], at(q), at(q_out), qs[0], qs[1], qos[0], qos[1],
-                            at(q_norm), at(k_norm), at(rope_freqs), at(positions), at(hists), at(hist_rows), q_heads, rot_dim,
-                            1 if rope_interleaved else 0, n_hists, rope_scale, eps)
-        _check(lib().sz_append_kv(kv, args, status.data_ptr(), s), "sz_append_kv")
-    return q_out, status
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _fail(st, where):
+    from . import SzError
+    raise SzError(st, where)
 
 
 def paged_attention(q, k_pages, v_pages, page_table, q_begin, kv_len, *, scale=None, causal=True, window=0, out=None,
@@ -192,28 +206,44 @@ def paged_attention(q, k_pages, v_pages, page_table, q_begin, kv_len, *, scale=N
 
     Returns (out, lse float32 [tokens, query heads] or None, status int32
     [requests])."""
-    torch = _torch()
-    tokens, dim, dtype = q.shape[0], k_pages.shape[-1], k_pages.dtype
-    kv = _pack_kv(torch, k_pages, v_pages, page_table, q_begin, kv_len, tokens)
-    qs, q_heads = _rows("q", q, dtype, tokens, dim), q.shape[1]
+    torch = _T or _load()
+    shape, dtype = k_pages.shape, k_pages.dtype
+    tokens, dim = q.shape[0], shape[-1]
+    kv = _pack_kv(torch, k_pages, v_pages, shape, page_table, q_begin, kv_len, tokens)
+    q_heads, q0, q1 = _rows("q", q, dtype, tokens, dim)
     if out is not None and out.shape != q.shape:
         raise ValueError("out of shape %s for q of %s" % (tuple(out.shape), tuple(q.shape)))
     if scale is None:
         scale = 1.0 / math.sqrt(dim)
     if window < 0 or window >= 1 << 32:
         raise ValueError("window must be 0 (none) or a number of keys below 2^32")
-    from . import _check, _nbytes, _workspace, lib, sz_plan_attention
-    with _On(torch, (k_pages, v_pages, q, page_table, q_begin, kv_len, out), stream) as (dev, s):
-        ws = _workspace(workspace, sz_plan_attention(dim), dev)
-        status = torch.empty(kv_len.shape[0], dtype=torch.int32, device=dev)
-        if out is None:
-            out = torch.empty((tokens, q_heads, dim), dtype=dtype, device=dev)
-        os_ = _rows("out", out, dtype, tokens, dim)
-        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=dev) if return_lse else None
-        args = _ATTENTION.pack(q.data_ptr(), out.data_ptr(), qs[0], qs[1], os_[0], os_[1], lse.data_ptr() if return_lse else 0, q_heads,
-                               1 if causal else 0, window, scale)
-        _check(lib().sz_paged_attention(kv, args, status.data_ptr(), ws.data_ptr(), _nbytes(ws), s), "sz_paged_attention")
-    return out, lse, status
+    dev = _device((k_pages, v_pages, q, page_table, q_begin, kv_len, out))
+
+    def call():
+        need = _attention_bytes(dim)
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty((need,), dtype=torch.uint8)
+        else:
+            from . import _workspace
+            _workspace(ws, need, q.device)
+        status = torch.empty_like(kv_len)
+        o = torch.empty_like(q) if out is None else out
+        _, o0, o1 = _rows("out", o, dtype, tokens, dim)
+        lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
+        args = _ATTENTION.pack(q.data_ptr(), o.data_ptr(), q0, q1, o0, o1, _at(lse), q_heads, 1 if causal else 0, window, scale)
+        st = _LIB.sz_paged_attention(kv, args, status.data_ptr(), ws.data_ptr(), ws.nbytes, _STREAM(dev))
+        if st:
+            _fail(st, "sz_paged_attention")
+        return o, lse, status
+
+    return _elsewhere(call, dev, stream) or call()
+
+
+@functools.lru_cache(maxsize=None)
+def _attention_bytes(dim):
+    from . import sz_plan_attention
+    return sz_plan_attention(dim)
 
 
 def rope_frequencies(rot_dim, base=10000.0, *, scaling=None, factor=1.0, trained_len=None, low_turns=1.0, high_turns=4.0, device=None):
@@ -226,7 +256,7 @@ def rope_frequencies(rot_dim, base=10000.0, *, scaling=None, factor=1.0, trained
     * ``scaling="bands"``: pairs that make fewer than low_turns turns over
       ``trained_len`` positions are divided by factor, pairs with more than
       high_turns are kept, and those between blend linearly in their turns."""
-    torch = _torch()
+    import torch
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
     t = torch.arange(0, rot_dim, 2, dtype=torch.float64)
