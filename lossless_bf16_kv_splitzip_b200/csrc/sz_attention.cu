@@ -161,27 +161,35 @@ constexpr int kPolyEvery = SZ_POLY;  // every so many pairs of weights take the 
 constexpr uint32_t kWholeTiles = 6;                     // blocks up to this long are not split when there is a CTA for each
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
+constexpr uint32_t kControlBytes = 768;                // of shared memory: barriers and the CTA's share
+
 template <int D, int kM>
 struct Shape {
     static constexpr int kTiles = kM, kHalves = D / 64;
+    // Rows of a row tile in use.  The products always take 128; with one row
+    // tile per CTA only 64 are filled (a few tokens per request), the others
+    // read whatever lies behind and their results are not looked at, which
+    // leaves room for a third key tile in flight.
+    static constexpr uint32_t kRows = kM == 2 ? 128 : 64;
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
     static constexpr int kQueries = D == 64 ? 2 : 1;  // blocks whose queries are in shared memory at a time
-    static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 4);
-    static constexpr int kSoftmaxThreads = kM * 128;
+    static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6);
+    static constexpr int kSoftmaxWarps = kRows / 32, kSoftmaxThreads = kM * kSoftmaxWarps * 32;  // warps per row tile
     static constexpr int kThreads = kSoftmaxThreads + 128;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
-    static constexpr uint32_t kQueryBytes = kM * kTileBytes;
-    static constexpr uint32_t kSmem = 1024 + kQueries * kQueryBytes + kSlots * kTileBytes;
+    static constexpr uint32_t kQueryHalf = kRows * kRowBytes, kQueryTile = kHalves * kQueryHalf, kQueryBytes = kM * kQueryTile;
+    static constexpr uint32_t kData = kQueries * kQueryBytes + kSlots * kTileBytes;
+    static constexpr uint32_t kSmem = kData + kControlBytes;
     // A part of a block: per row tile 4 channels of all rows, the next 4, ...
     // (so that threads that hold a row each write and read side by side),
     // then (m, l) per row.
-    static constexpr uint32_t kPartFloats = kM * kTileRows * (D + 2);
+    static constexpr uint32_t kPartFloats = kM * kRows * (D + 2);
     static __host__ __device__ constexpr uint32_t part_o(uint32_t m_tile, uint32_t chunk, uint32_t row) {
-        return ((m_tile * (D / 4) + chunk) * kTileRows + row) * 4;
+        return ((m_tile * (D / 4) + chunk) * kRows + row) * 4;
     }
     static __host__ __device__ constexpr uint32_t part_ml(uint32_t m_tile, uint32_t row) {
-        return kM * kTileRows * D + (m_tile * kTileRows + row) * 2;
+        return kM * kRows * D + (m_tile * kRows + row) * 2;
     }
 };
 
@@ -352,8 +360,8 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
 }
 
 struct PlanShared {
-    uint64_t warp_units[16], warp_blocks[16];
-    uint32_t warp_most[16];
+    uint64_t warp_units[12], warp_blocks[12];
+    uint32_t warp_most[12];
     uint64_t total;
     uint64_t first, left;  // this CTA's units
     uint32_t used;         // CTAs with work
@@ -511,6 +519,13 @@ struct Bars {
     uint64_t drain;
 };
 
+struct Control {  // behind the tiles in shared memory
+    Bars bars;
+    PlanShared plan;
+    uint32_t tmem, failed;
+};
+static_assert(sizeof(Control) <= kControlBytes, "control block");
+
 template <typename T, int D, int kM>
 __global__ void __launch_bounds__(Shape<D, kM>::kThreads, Shape<D, kM>::kCtasPerSm)
 attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ CUtensorMap q_map,
@@ -519,20 +534,20 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t kScoreWord = mma_word(kBf16, 128, false);
     constexpr uint32_t kOutWord = mma_word(kBf16, D, true);
-    extern __shared__ uint8_t raw[];
-    __shared__ Bars bars;
-    __shared__ PlanShared plan;
-    __shared__ uint32_t tmem_base_s;
-    __shared__ uint32_t failed;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Control &control = *reinterpret_cast<Control *>(raw + S::kData);
+    Bars &bars = control.bars;
+    PlanShared &plan = control.plan;
+    uint32_t &failed = control.failed;
     // what is the same for a whole warp is passed through a shuffle, so that
     // the compiler keeps it in uniform registers, where the tensor
     // instructions want their operands
     const uint32_t tid = threadIdx.x, wid = same(tid >> 5), lane = tid & 31;
-    const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t smem0 = smem_u32(raw);
     const uint32_t ring0 = smem0 + S::kQueries * S::kQueryBytes;
-    constexpr uint32_t kMmaWarp = kM * 4, kCopyWarp = kM * 4 + 1, kStatusWarp = kM * 4 + 3;
+    constexpr uint32_t kMmaWarp = kM * S::kSoftmaxWarps, kCopyWarp = kMmaWarp + 1, kStatusWarp = kMmaWarp + 3;
 
-    if (wid == kMmaWarp) tmem_alloc(&tmem_base_s, S::kColumns);
+    if (wid == kMmaWarp) tmem_alloc(&control.tmem, S::kColumns);
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&bars.full[i], 1);
@@ -544,8 +559,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         }
         for (int x = 0; x < kM; ++x) {
             mbar_init(&bars.s_full[x], 1);
-            mbar_init(&bars.p_full[x][0], 4);
-            mbar_init(&bars.p_full[x][1], 4);
+            mbar_init(&bars.p_full[x][0], S::kSoftmaxWarps);
+            mbar_init(&bars.p_full[x][1], S::kSoftmaxWarps);
             mbar_init(&bars.pv_done[x], 1);
         }
         mbar_init(&bars.drain, 1);
@@ -570,7 +585,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     allow_dependents();
-    const uint32_t tmem = same(tmem_base_s);
+    const uint32_t tmem = same(control.tmem);
     Cursor cur;
     cur.r = plan.r;
     cur.head = plan.head;
@@ -636,7 +651,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         for (uint32_t x = 0; x < tiles; ++x)
 #pragma unroll
                             for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
-                                tma_load_3d(smem0 + buf * S::kQueryBytes + x * S::kTileBytes + hf * kHalfBytes, &q_map, (int)(hf * 64), (int)(head * p.group),
+                                tma_load_3d(smem0 + buf * S::kQueryBytes + x * S::kQueryTile + hf * S::kQueryHalf, &q_map, (int)(hf * 64), (int)(head * p.group),
                                             (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full[buf]));
                 }
                 __syncwarp();
@@ -699,12 +714,12 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             return same(have ? 1u : 0u) != 0;
         };
         auto score = [&](uint32_t m, uint32_t at, uint32_t buf) {  // S_m = Q_m K^T
-            const uint32_t a = q_lo + buf * (S::kQueryBytes >> 4) + m * (S::kTileBytes >> 4), b = k_lo + at * (S::kTileBytes >> 4);
+            const uint32_t a = q_lo + buf * (S::kQueryBytes >> 4) + m * (S::kQueryTile >> 4), b = k_lo + at * (S::kTileBytes >> 4);
             if (one) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = ((uint32_t)(i / 4) * kHalfBytes + (uint32_t)(i % 4) * 32) >> 4;
-                    mma_smem(tmem + m * 128, full_desc(a + off), full_desc(b + off), kScoreWord, i > 0);
+                    const uint32_t half = (uint32_t)(i / 4), off = (uint32_t)(i % 4) * 32 >> 4;
+                    mma_smem(tmem + m * 128, full_desc(a + half * (S::kQueryHalf >> 4) + off), full_desc(b + half * (kHalfBytes >> 4) + off), kScoreWord, i > 0);
                 }
                 mma_commit(&bars.s_full[m]);
             }
@@ -817,9 +832,9 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     } else {
         // ----------------------------------------------------------- softmax
 
-        const uint32_t m_tile = wid / 4;
-        const uint32_t row = tid & 127;
-        const uint32_t lanes = (wid & 3) * 32;  // this warp's lanes of tensor memory
+        const uint32_t m_tile = wid / S::kSoftmaxWarps;
+        const uint32_t row = tid % S::kRows;
+        const uint32_t lanes = wid % S::kSoftmaxWarps * 32;  // this warp's lanes of tensor memory
         const uint32_t s_at = tmem + (lanes << 16) + m_tile * 128;
         const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D;
         const uint32_t my_token = row / p.group, my_head = row % p.group;
@@ -1151,7 +1166,7 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     p.c = a.scale * kLog2e;
     if (!(p.c > 1e-37f)) p.c = 1e-37f;  // a hidden score is -inf, and -inf * 0 would be NaN
     p.group = a.q_heads / kv.heads;
-    p.tile_tokens = kTileRows / p.group;
+    p.tile_tokens = S::kRows / p.group;
     p.box_tokens = umin32(kv.page_tokens, kTileRows);
     p.copies = kTileRows / p.box_tokens;
     p.key_tile = p.copies * p.box_tokens;
@@ -1191,10 +1206,10 @@ static cudaError_t launch_attention_t(const sz_paged_kv &kv, const sz_attention_
                                       cudaStream_t s) {
     if (!tensor_shape(kv, a)) return launch_any_t<T>(kv, a, status, s);
     // Two row tiles per CTA share a key tile; with no more rows per request
-    // than one tile holds (on average: the lengths are on the device), two
-    // CTAs per SM of one row tile each keep more copies in flight.
-    const uint64_t rows = kv.n_tokens * (a.q_heads / kv.heads);
-    const bool two = rows > (uint64_t)kv.n_reqs * kTileRows;
+    // than one short tile holds (on average: the lengths are on the device),
+    // two CTAs per SM of one row tile each keep more copies in flight.
+    const uint64_t group = a.q_heads / kv.heads, rows = kv.n_tokens * group;
+    const bool two = rows > (uint64_t)kv.n_reqs * 64 || group > 64;
     if (kv.head_dim == 128)
         return two ? launch_tensor<T, 128, 2>(kv, a, status, ws, dev, s) : launch_tensor<T, 128, 1>(kv, a, status, ws, dev, s);
     return two ? launch_tensor<T, 64, 2>(kv, a, status, ws, dev, s) : launch_tensor<T, 64, 1>(kv, a, status, ws, dev, s);
