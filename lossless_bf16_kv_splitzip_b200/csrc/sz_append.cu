@@ -4,192 +4,350 @@
 //
 // Mathematics.  For a head x of D channels: y = x * w / sqrt(mean(x^2) + eps);
 // the first R channels are R/2 pairs (a, b) turned by pos * f_t:
-// (a cos - b sin, b cos + a sin) * scale.  A pair's partner sits R/2 channels
-// away (or next to it when interleaved), so a head held 8 channels per lane
-// needs one exchange of 16 bytes per lane.
+// (a cos - b sin, b cos + a sin) * scale.  A lane holds two runs of four
+// channels that are four whole pairs -- R/2 channels apart, or side by side
+// when pairs are adjacent -- so that turning needs no exchange between lanes.
 //
 // Bound: memory.  Every value is read once and written once, 4 bytes each.
-//
-// One block per new token: its angles are computed once (a double product,
-// reduced by whole turns in double so that a position of millions keeps its
-// angle, then a 32-bit sine and cosine) and serve all of its heads.
+// A warp takes one token and a run of its heads (D = 128: two heads at a
+// time, two 8-byte loads per lane), kBatch heads' loads under way per lane;
+// nothing but the counts needs other warps.  The first loads are issued before the token's
+// request, page and angles are looked up, which is a chain of dependent loads.
+// A token's angles are computed once per warp (a double product, reduced by
+// whole turns in double so that a position of millions keeps its angle, then
+// a 32-bit sine and cosine) and serve all of its heads.
 #include "sz_paged.cuh"
 
 namespace sz {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = 8, kAppendThreads = 32 * kAppendWarps;
 constexpr uint32_t kMaxHeadDim = 256;
+constexpr int kBatch = 4;  // head groups whose loads a warp has under way
 
-// 8 channels of one lane's chunk, partners exchanged: returns y turned.
-// `chunk` = channels 8*chunk ..; half layout: the partner chunk lies
-// half_chunks away inside the rotated part.
-__device__ __forceinline__ void rotate8(float (&y)[8], const float (&partner)[8], const float2 *cs, uint32_t chunk,
-                                        uint32_t half_chunks, bool interleaved, float scale) {
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 c = cs[chunk * 4 + i];
-            const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = (a * c.x - b * c.y) * scale;
-            y[2 * i + 1] = (b * c.x + a * c.y) * scale;
-        }
-    } else {
-        const bool second = chunk >= half_chunks;
-        const uint32_t t0 = (second ? chunk - half_chunks : chunk) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 c = cs[t0 + i];
-            const float s = second ? c.y : -c.y;
-            y[i] = (y[i] * c.x + partner[i] * s) * scale;
-        }
+struct AppendArgs {
+    sz_paged_kv kv;
+    sz_append_args a;
+    int32_t *status;
+    uint32_t tokens_per_block;
+    uint32_t slice_heads;  // heads a block takes of each of its tokens (without counts)
+};
+
+// The request that owns row `token`, or n_reqs, by one warp: 32 entries of
+// q_begin are compared at a time, so that n requests take log32(n) rounds.
+__device__ __forceinline__ uint32_t warp_request_of(const sz_paged_kv &kv, uint32_t token, uint32_t lane) {
+    uint32_t lo = 0, n = kv.n_reqs;  // the answer, if any, is in [lo, lo + n)
+    while (n > 1) {
+        const uint32_t step = (n + 31) / 32;
+        const uint32_t at = lo + lane * step;
+        const bool before = lane * step < n && __ldg(kv.d_q_begin + at) <= (int32_t)token;
+        const uint32_t hits = __ballot_sync(0xFFFFFFFFu, before);
+        if (hits == 0) return kv.n_reqs;
+        const uint32_t last = 31 - __clz(hits);  // the largest sample at or before the token
+        n = umin32(step, n - last * step);
+        lo += last * step;
     }
+    return lo;
 }
 
-template <typename T, int kLanes>  // kLanes lanes hold one head, 8 channels each
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(sz_paged_kv kv, sz_append_args a, int32_t *status) {
-    __shared__ float2 cs[kMaxHeadDim / 2];
-    const uint32_t tid = threadIdx.x;
-    const uint32_t D = kv.head_dim;
-    const uint32_t chunks = D / 8;
+// Where a token's keys and values go.
+struct Place {
+    uint32_t r;     // n_reqs: nowhere
+    uint32_t place;  // position in the cache
+    int32_t page;
+    uint32_t slot;
+};
+__device__ __forceinline__ Place token_place(const AppendArgs &p, uint32_t token, uint32_t lane) {
+    Place x;
+    x.r = warp_request_of(p.kv, token, lane);
+    x.page = -1;
+    x.place = x.slot = 0;
+    if (x.r >= p.kv.n_reqs) return x;
+    const Request q = load_request(p.kv, x.r);
+    if (q.status != SZ_OK || q.n > q.kv || token < (uint32_t)q.q0 || token >= (uint32_t)(q.q0 + q.n)) {
+        x.r = p.kv.n_reqs;
+        return x;
+    }
+    x.place = (uint32_t)(q.kv - q.n) + (token - (uint32_t)q.q0);
+    x.slot = x.place % p.kv.page_tokens;
+    x.page = page_of(p.kv, x.r, x.place / p.kv.page_tokens);
+    if (x.page < 0) x.r = p.kv.n_reqs;
+    return x;
+}
 
-    // ---- the requests' statuses: warps of the grid take one request each
-    {
-        const uint32_t warps = gridDim.x * (kAppendThreads / 32);
-        for (uint32_t r = blockIdx.x * (kAppendThreads / 32) + (tid >> 5); r < kv.n_reqs; r += warps) {
-            const Request q = load_request(kv, r);
-            sz_status st = q.status;
-            if (st == SZ_OK && q.n > q.kv) st = SZ_ERR_INVALID;
-            if (st == SZ_OK && q.n > 0) {
-                st = check_pages(kv, r, (uint32_t)(q.kv - q.n) / kv.page_tokens, (uint32_t)(q.kv - 1) / kv.page_tokens + 1);
-                if (a.d_hists_or_null) {
-                    const uint32_t kr = a.d_hist_rows_or_null ? a.d_hist_rows_or_null[r] : r;
-                    const uint32_t vr = a.d_hist_rows_or_null ? a.d_hist_rows_or_null[kv.n_reqs + r] : kv.n_reqs + r;
-                    if (kr >= a.n_hists || vr >= a.n_hists) st = SZ_ERR_INVALID;
-                }
-            }
-            if ((tid & 31) == 0) status[r] = st;
-        }
-    }
-    if (blockIdx.x >= kv.n_tokens) return;
-    const uint32_t token = blockIdx.x;
-    const uint32_t r = request_of(kv, token);
-    if (r >= kv.n_reqs) return;
-    const Request q = load_request(kv, r);
-    if (q.status != SZ_OK || q.n > q.kv) return;
-    const uint32_t place = (uint32_t)(q.kv - q.n) + (token - (uint32_t)q.q0);
-    const int32_t page = page_of(kv, r, place / kv.page_tokens);
-    if (page < 0) return;
-    uint32_t hk = 0xFFFFFFFFu, hv = 0xFFFFFFFFu;
-    if (a.d_hists_or_null) {
-        hk = a.d_hist_rows_or_null ? a.d_hist_rows_or_null[r] : r;
-        hv = a.d_hist_rows_or_null ? a.d_hist_rows_or_null[kv.n_reqs + r] : kv.n_reqs + r;
-        if (hk >= a.n_hists || hv >= a.n_hists) return;
-    }
-    if (a.rot_dim) {
-        const double pos = a.d_positions_or_null ? (double)a.d_positions_or_null[token] : (double)place;
-        for (uint32_t t = tid; t < a.rot_dim / 2; t += kAppendThreads) {
-            double turns = pos * a.d_freqs_or_null[t] * 0.15915494309189533577;
-            turns -= rint(turns);
-            float s, c;
-            sincospif(2.0f * (float)turns, &s, &c);
-            cs[t] = make_float2(c, s);
-        }
-    }
-    __syncthreads();
+// Rows of the histograms that request r's keys and values go to; false when
+// one is out of range.
+__device__ __forceinline__ bool hist_rows(const AppendArgs &p, uint32_t r, uint32_t &k_row, uint32_t &v_row) {
+    k_row = p.a.d_hist_rows_or_null ? p.a.d_hist_rows_or_null[r] : r;
+    v_row = p.a.d_hist_rows_or_null ? p.a.d_hist_rows_or_null[p.kv.n_reqs + r] : p.kv.n_reqs + r;
+    return k_row < p.a.n_hists && v_row < p.a.n_hists;
+}
 
-    const uint32_t lane = tid % kLanes, group = tid / kLanes;
-    const uint32_t n_heads = a.q_heads + 2 * kv.heads;
-    const uint32_t slot = place % kv.page_tokens;
-    const uint32_t half_chunks = a.rot_dim / 16;
-    for (uint32_t h0 = 0; h0 < n_heads; h0 += kAppendThreads / kLanes) {
-        const uint32_t h = h0 + group;
-        const bool live = h < n_heads && lane < chunks;
-        const uint16_t *src = nullptr;
-        uint16_t *dst = nullptr;
-        const uint16_t *w = nullptr;
-        bool turn = false, is_k = false, is_v = false;
-        if (h < a.q_heads) {
-            src = (const uint16_t *)a.d_q_or_null + token * a.q_stride[0] + h * a.q_stride[1];
-            dst = (uint16_t *)a.d_q_out + token * a.q_out_stride[0] + h * a.q_out_stride[1];
-            w = (const uint16_t *)a.d_q_norm_or_null;
-            turn = true;
-        } else if (h < a.q_heads + kv.heads) {
-            const uint32_t g = h - a.q_heads;
-            src = (const uint16_t *)a.d_k + token * a.k_stride[0] + g * a.k_stride[1];
-            dst = (uint16_t *)kv.d_k + (uint64_t)page * kv.k_stride[0] + g * kv.k_stride[1] + slot * kv.k_stride[2];
-            w = (const uint16_t *)a.d_k_norm_or_null;
-            turn = is_k = true;
-        } else if (h < n_heads) {
-            const uint32_t g = h - a.q_heads - kv.heads;
-            src = (const uint16_t *)a.d_v + token * a.v_stride[0] + g * a.v_stride[1];
-            dst = (uint16_t *)kv.d_v + (uint64_t)page * kv.v_stride[0] + g * kv.v_stride[1] + slot * kv.v_stride[2];
-            is_v = true;
-        }
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = ld_stream_v4(src + lane * 8);
-        uint4 out = raw;
-        // The exchange needs every lane of the warp: it is made whatever the
-        // head, and used by the lanes whose head turns.
-        float y[8];
-        widen8<T>(raw, y);
-        float f = 1.0f;
-        {
-            float sum = 0.0f;
+// Exponent counts of a block: 256 bins x 32 lane columns, bin-major, so that
+// the lanes of a warp never meet in a bank whatever exponents they hold.
+__device__ __forceinline__ void count2(uint2 v, uint32_t column) {
+    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += y[i] * y[i];
-#pragma unroll
-            for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            if (w) f = rsqrtf(sum / (float)D + a.eps);
-        }
-        if (w && live) {
-            float ww[8];
-            widen8<T>(__ldg((const uint4 *)(w + lane * 8)), ww);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= f * ww[i];
-        }
-        float partner[8];
-        const uint32_t other = lane < half_chunks ? lane + half_chunks : lane - half_chunks;
-        if (!a.interleaved && a.rot_dim) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) partner[i] = __shfl_sync(0xFFFFFFFFu, y[i], other, kLanes);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) partner[i] = 0.0f;
-        }
-        if (live && turn) {
-            if (lane * 8 < a.rot_dim) rotate8(y, partner, cs, lane, half_chunks, a.interleaved != 0, a.rot_scale);
-            if (w || a.rot_dim) out = narrow8<T>(y);
-        }
-        if (live) {
-            *reinterpret_cast<uint4 *>(dst + lane * 8) = out;
-            if (a.d_hists_or_null && (is_k || is_v)) {
-                uint32_t *row = a.d_hists_or_null + (uint64_t)(is_k ? hk : hv) * 256;
-                const uint32_t ws[4] = {out.x, out.y, out.z, out.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    atomicAdd(row + ((ws[i] >> 7) & 0xFFu), 1u);
-                    atomicAdd(row + ((ws[i] >> 23) & 0xFFu), 1u);
-                }
-            }
-        }
+    for (int i = 0; i < 2; ++i) {
+        // the exponent sits in bits 7..14 of each half: exponent * 128 is the row's byte offset
+        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(column + (w[i] & 0x7F80u)) : "memory");
+        asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(column + ((w[i] >> 16) & 0x7F80u)) : "memory");
     }
 }
 
 template <typename T>
-static cudaError_t launch_append_t(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, cudaStream_t s) {
-    const uint32_t grid = (uint32_t)umax64(kv.n_tokens, div_up(kv.n_reqs, kAppendThreads / 32));
-    if (kv.head_dim <= 64)
-        append_kernel<T, 8><<<grid, kAppendThreads, 0, s>>>(kv, a, status);
-    else if (kv.head_dim <= 128)
-        append_kernel<T, 16><<<grid, kAppendThreads, 0, s>>>(kv, a, status);
-    else
-        append_kernel<T, 32><<<grid, kAppendThreads, 0, s>>>(kv, a, status);
+__device__ __forceinline__ void widen4(uint2 v, float (&x)[4]) {
+    const float2 a = Half2<T>::widen(v.x), b = Half2<T>::widen(v.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+template <typename T>
+__device__ __forceinline__ uint2 narrow4(float a, float b, float c, float d) {
+    return make_uint2(Half2<T>::narrow(a, b), Half2<T>::narrow(c, d));
+}
+__device__ __forceinline__ uint2 ld_stream_v2(const void *p) { return __ldcs(reinterpret_cast<const uint2 *>(p)); }
+
+// One token's heads [h_begin, h_end) by one warp; kLanes lanes hold one head.
+template <typename T, int kLanes, bool kAdjacent, bool kCount>
+__device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token, uint32_t h_begin, uint32_t h_end, uint32_t lane,
+                                             float2 *cs, uint32_t column) {
+    constexpr uint32_t kHeads = 32 / kLanes;  // at a time
+    const sz_paged_kv &kv = p.kv;
+    const sz_append_args &a = p.a;
+    const uint32_t D = kv.head_dim, l = lane % kLanes, group = lane / kLanes;
+    const uint32_t pairs = a.rot_dim / 2, turning = pairs / 4;  // lanes whose channels turn
+    const bool in_head = l * 8 < D, turns_here = l < turning;
+    // this lane's two runs of four channels
+    const uint32_t c0 = kAdjacent ? l * 8 : turns_here ? l * 4 : l * 8;
+    const uint32_t c1 = kAdjacent || !turns_here ? c0 + 4 : c0 + pairs;
+    float cos4[4], sin4[4];
+    Place at;
+    at.r = kv.n_reqs + 1;  // not looked up
+    at.page = at.slot = at.place = 0;
+#pragma unroll 1
+    for (uint32_t segment = 0; segment < 3; ++segment) {  // queries, keys, values
+        const uint32_t s_begin = segment == 0 ? 0 : a.q_heads + (segment - 1) * kv.heads;
+        const uint32_t s_heads = segment == 0 ? a.q_heads : kv.heads;
+        const uint32_t from = h_begin > s_begin ? h_begin - s_begin : 0;
+        const uint32_t to = h_end > s_begin ? umin32(h_end - s_begin, s_heads) : 0;  // of the segment's heads
+        if (from >= to) continue;
+        const uint16_t *src = (const uint16_t *)(segment == 0 ? a.d_q_or_null : segment == 1 ? a.d_k : a.d_v);
+        const uint64_t *const ss = segment == 0 ? a.q_stride : segment == 1 ? a.k_stride : a.v_stride;
+        const uint64_t src_head = ss[1];
+        src += token * ss[0] + (from + group) * src_head;
+        const uint16_t *const w = (const uint16_t *)(segment == 0 ? a.d_q_norm_or_null : segment == 1 ? a.d_k_norm_or_null : nullptr);
+        uint16_t *dst = nullptr;
+        uint64_t dst_head = 0;
+        for (uint32_t h0 = from; h0 < to; h0 += kBatch * kHeads) {
+            uint2 x0[kBatch], x1[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                x0[i] = x1[i] = make_uint2(0, 0);
+                if (h0 + i * kHeads + group < to && in_head) {
+                    x0[i] = ld_stream_v2(src + i * (kHeads * src_head) + c0);
+                    x1[i] = ld_stream_v2(src + i * (kHeads * src_head) + c1);
+                }
+            }
+            src += kBatch * kHeads * src_head;
+            if (at.r > kv.n_reqs) {  // once, with loads under way
+                at = token_place(p, token, lane);
+                if (at.r >= kv.n_reqs) return;
+                if (pairs && segment < 2) {
+                    const double pos = a.d_positions_or_null ? (double)a.d_positions_or_null[token] : (double)at.place;
+                    __syncwarp();  // the last token's angles have been read
+                    for (uint32_t t = lane; t < pairs; t += 32) {
+                        double turns = pos * a.d_freqs_or_null[t] * 0.15915494309189533577;
+                        turns -= rint(turns);
+                        float sn, cn;
+                        sincospif(2.0f * (float)turns, &sn, &cn);
+                        cs[t] = make_float2(cn * a.rot_scale, sn * a.rot_scale);
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = pairs && segment < 2 && turns_here ? cs[l * 4 + i] : make_float2(1.0f, 0.0f);
+                    cos4[i] = y.x;
+                    sin4[i] = y.y;
+                }
+            }
+            if (dst == nullptr) {
+                if (segment == 0) {
+                    dst = (uint16_t *)a.d_q_out + token * a.q_out_stride[0];
+                    dst_head = a.q_out_stride[1];
+                } else {
+                    const uint64_t *const ds = segment == 1 ? kv.k_stride : kv.v_stride;
+                    dst = (uint16_t *)(segment == 1 ? kv.d_k : kv.d_v) + (uint64_t)at.page * ds[0] + at.slot * ds[2];
+                    dst_head = ds[1];
+                }
+                dst += (from + group) * dst_head;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (h0 + i * kHeads >= to) break;
+                const bool live = h0 + i * kHeads + group < to && in_head;
+                uint2 y0 = x0[i], y1 = x1[i];
+                if (w || (pairs && segment < 2)) {
+                    float u[4], v[4];
+                    widen4<T>(y0, u);
+                    widen4<T>(y1, v);
+                    if (w) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sum += u[e] * u[e] + v[e] * v[e];
+#pragma unroll
+                        for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                        const float f = rsqrtf(sum / (float)D + a.eps);
+                        float wu[4] = {}, wv[4] = {};
+                        if (in_head) {
+                            widen4<T>(__ldg((const uint2 *)(w + c0)), wu);
+                            widen4<T>(__ldg((const uint2 *)(w + c1)), wv);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] *= f * wu[e], v[e] *= f * wv[e];
+                    }
+                    if (turns_here) {
+                        // pair i: (u[i], v[i]), or neighbours in u then v
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float &a_ = kAdjacent ? (e < 2 ? u[2 * e] : v[2 * e - 4]) : u[e];
+                            float &b_ = kAdjacent ? (e < 2 ? u[2 * e + 1] : v[2 * e - 3]) : v[e];
+                            const float turned = a_ * cos4[e] - b_ * sin4[e];
+                            b_ = b_ * cos4[e] + a_ * sin4[e];
+                            a_ = turned;
+                        }
+                    }
+                    y0 = narrow4<T>(u[0], u[1], u[2], u[3]);
+                    y1 = narrow4<T>(v[0], v[1], v[2], v[3]);
+                }
+                if (live) {
+                    *reinterpret_cast<uint2 *>(dst + i * (kHeads * dst_head) + c0) = y0;
+                    *reinterpret_cast<uint2 *>(dst + i * (kHeads * dst_head) + c1) = y1;
+                    if (kCount && segment > 0) {
+                        count2(y0, column);
+                        count2(y1, column);
+                    }
+                }
+            }
+            dst += kBatch * kHeads * dst_head;
+        }
+    }
+}
+
+template <typename T, int kLanes, bool kAdjacent, bool kCount>
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendArgs p) {
+    __shared__ float2 cs[kAppendWarps][kMaxHeadDim / 2];
+    __shared__ uint32_t columns[kCount ? 256 * 32 : 1];
+    const sz_paged_kv &kv = p.kv;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+
+    // ---- the requests' statuses: warps of the first row of blocks take one each
+    if (blockIdx.y == 0) {
+        for (uint32_t r = blockIdx.x * kAppendWarps + wid; r < kv.n_reqs; r += gridDim.x * kAppendWarps) {
+            const Request q = load_request(kv, r);
+            sz_status st = q.status;
+            uint32_t k_row, v_row;
+            if (st == SZ_OK && q.n > q.kv) st = SZ_ERR_INVALID;
+            if (st == SZ_OK && q.n > 0) {
+                st = check_pages(kv, r, (uint32_t)(q.kv - q.n) / kv.page_tokens, (uint32_t)(q.kv - 1) / kv.page_tokens + 1);
+                if (kCount && !hist_rows(p, r, k_row, v_row)) st = SZ_ERR_INVALID;
+            }
+            if (lane == 0) p.status[r] = st;
+        }
+    }
+    const uint32_t t_begin = blockIdx.x * p.tokens_per_block;
+    const uint32_t t_end = (uint32_t)umin64(kv.n_tokens, (uint64_t)t_begin + p.tokens_per_block);
+    const uint32_t all = p.a.q_heads + 2 * kv.heads;
+    if constexpr (!kCount) {
+        const uint32_t h_begin = blockIdx.y * p.slice_heads, h_end = umin32(all, h_begin + p.slice_heads);
+        for (uint32_t t = t_begin + wid; t < t_end; t += kAppendWarps)
+            append_token<T, kLanes, kAdjacent, false>(p, t, h_begin, h_end, lane, cs[wid], 0);
+    } else {
+        // Block rows: keys, values and (if any) queries.  The counts of a
+        // request's tokens are added to its row before the next request's.
+        const bool is_q = blockIdx.y == 2, is_v = blockIdx.y == 1;
+        const uint32_t h_begin = is_q ? 0 : p.a.q_heads + (is_v ? kv.heads : 0);
+        const uint32_t h_end = is_q ? p.a.q_heads : h_begin + kv.heads;
+        if (!is_q) {
+            for (uint32_t i = tid; i < 256 * 32 / 4; i += kAppendThreads) reinterpret_cast<uint4 *>(columns)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+        }
+        const uint32_t column = smem_u32(columns) + 4 * lane;
+        uint32_t t = t_begin;
+        while (t < t_end) {  // the same run of tokens in every warp
+            const uint32_t r = warp_request_of(kv, t, lane);
+            uint32_t stop = t_end, k_row = 0, v_row = 0;
+            bool counted = false;
+            if (r < kv.n_reqs) {
+                const Request q = load_request(kv, r);
+                if (q.status == SZ_OK && t >= (uint32_t)q.q0 && t < (uint32_t)(q.q0 + q.n)) {
+                    stop = umin32(t_end, (uint32_t)(q.q0 + q.n));
+                    counted = hist_rows(p, r, k_row, v_row);
+                } else {
+                    stop = t + 1;  // a row of no request
+                }
+            }
+            if (counted) {
+                for (uint32_t i = t + wid; i < stop; i += kAppendWarps)
+                    if (is_q)
+                        append_token<T, kLanes, kAdjacent, false>(p, i, h_begin, h_end, lane, cs[wid], 0);
+                    else
+                        append_token<T, kLanes, kAdjacent, true>(p, i, h_begin, h_end, lane, cs[wid], column);
+                if (!is_q) {
+                    __syncthreads();
+                    uint32_t sum = 0;  // thread = bin; its 32 columns from another start in every lane
+#pragma unroll 8
+                    for (uint32_t i = 0; i < 32; ++i) {
+                        uint32_t &x = columns[tid * 32 + ((i + lane) & 31)];
+                        sum += x;
+                        x = 0;
+                    }
+                    if (sum) atomicAdd(p.a.d_hists_or_null + (uint64_t)(is_v ? v_row : k_row) * 256 + tid, sum);
+                    __syncthreads();
+                }
+            }
+            t = stop;
+        }
+    }
+}
+
+template <typename T, int kLanes, bool kAdjacent>
+static cudaError_t launch_append_lanes(AppendArgs &p, int sms, cudaStream_t s) {
+    const uint32_t heads = p.a.q_heads + 2 * p.kv.heads, at_once = 32 / kLanes;
+    const uint64_t tokens = p.kv.n_tokens;
+    if (p.a.d_hists_or_null) {
+        // Counts cost a pass over 32 KB of shared memory per block and request:
+        // about four blocks per SM in all, of at least a token per warp.
+        const uint64_t want = umax64(1, (uint64_t)sms * 4 / 2);
+        p.tokens_per_block = (uint32_t)umax64(kAppendWarps, div_up(tokens, want));
+        const dim3 grid((uint32_t)umax64(1, div_up(tokens, p.tokens_per_block)), p.a.q_heads ? 3 : 2);
+        append_kernel<T, kLanes, kAdjacent, true><<<grid, kAppendThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    // A warp takes a token's heads in slices: as many warps as keep the SMs
+    // busy (24 each), and no more, since each looks its token up anew.
+    const uint64_t groups = div_up(heads, at_once);
+    const uint64_t per_warp = umax64(1, tokens * groups / ((uint64_t)sms * 24));
+    p.slice_heads = (uint32_t)umin64(groups, per_warp) * at_once;
+    p.tokens_per_block = kAppendWarps;
+    const dim3 grid((uint32_t)umax64(1, div_up(tokens, kAppendWarps)), (uint32_t)div_up(heads, p.slice_heads));
+    append_kernel<T, kLanes, kAdjacent, false><<<grid, kAppendThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_append(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, cudaStream_t s) {
-    return kv.dtype == SZ_BF16 ? launch_append_t<__nv_bfloat16>(kv, a, status, s)
-                               : launch_append_t<__half>(kv, a, status, s);
+template <typename T, bool kAdjacent>
+static cudaError_t launch_append_t(AppendArgs &p, int sms, cudaStream_t s) {
+    if (p.kv.head_dim <= 64) return launch_append_lanes<T, 8, kAdjacent>(p, sms, s);
+    if (p.kv.head_dim <= 128) return launch_append_lanes<T, 16, kAdjacent>(p, sms, s);
+    return launch_append_lanes<T, 32, kAdjacent>(p, sms, s);
+}
+
+cudaError_t launch_append(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, int sms, cudaStream_t s) {
+    AppendArgs p{};
+    p.kv = kv;
+    p.a = a;
+    p.status = status;
+    if (kv.dtype == SZ_BF16)
+        return a.interleaved ? launch_append_t<__nv_bfloat16, true>(p, sms, s) : launch_append_t<__nv_bfloat16, false>(p, sms, s);
+    return a.interleaved ? launch_append_t<__half, true>(p, sms, s) : launch_append_t<__half, false>(p, sms, s);
 }
 
 }  // namespace sz

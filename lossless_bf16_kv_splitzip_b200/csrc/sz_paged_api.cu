@@ -5,7 +5,7 @@
 
 namespace sz {
 
-cudaError_t launch_append(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, cudaStream_t s);
+cudaError_t launch_append(const sz_paged_kv &kv, const sz_append_args &a, int32_t *status, int sms, cudaStream_t s);
 cudaError_t launch_attention(const sz_paged_kv &kv, const sz_attention_args &a, int32_t *status, void *ws, const DeviceInfo &dev,
                              cudaStream_t s);
 uint64_t attention_workspace(uint32_t head_dim);
@@ -103,7 +103,9 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *a, int32_t *
         !aligned(a->d_positions_or_null, 8) || !aligned(a->d_hists_or_null, 4) || !aligned(a->d_hist_rows_or_null, 4) ||
         !aligned(d_status, 4))
         return SZ_ERR_ALIGN;
-    const cudaError_t e = launch_append(*kv, *a, d_status, static_cast<cudaStream_t>(stream));
+    DeviceInfo dev;
+    if (const sz_status st = device_info(dev)) return st;
+    const cudaError_t e = launch_append(*kv, *a, d_status, dev.sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SZ_OK : SZ_ERR_CUDA;
 }
 
