@@ -16,11 +16,15 @@
 // A token's angles are computed once per warp (a double product, reduced by
 // whole turns in double so that a position of millions keeps its angle, then
 // a 32-bit sine and cosine) and serve all of its heads.
+#include <type_traits>
+
 #include "sz_paged.cuh"
 
 namespace sz {
 
-constexpr int kAppendWarps = 8, kAppendThreads = 32 * kAppendWarps;
+// Warps per block: few without counts, so that blocks spread evenly over the
+// SMs; with counts as many threads as bins.
+constexpr int kAppendWarps = 4, kCountWarps = 8;
 constexpr uint32_t kMaxHeadDim = 256;
 constexpr int kBatch = 4;  // head groups whose loads a warp has under way
 
@@ -56,6 +60,19 @@ struct Place {
     int32_t page;
     uint32_t slot;
 };
+__device__ __forceinline__ Place place_in(const AppendArgs &p, uint32_t r, const Request &q, uint32_t token) {
+    Place x;
+    x.r = r;
+    x.place = (uint32_t)(q.kv - q.n) + (token - (uint32_t)q.q0);
+    x.slot = x.place % p.kv.page_tokens;
+    x.page = page_of(p.kv, r, x.place / p.kv.page_tokens);
+    if (x.page < 0) x.r = p.kv.n_reqs;
+    return x;
+}
+// Whether row `token` is one of request q's, and q one that can be written.
+__device__ __forceinline__ bool owns(const Request &q, uint32_t token) {
+    return q.status == SZ_OK && q.n <= q.kv && token >= (uint32_t)q.q0 && token < (uint32_t)(q.q0 + q.n);
+}
 __device__ __forceinline__ Place token_place(const AppendArgs &p, uint32_t token, uint32_t lane) {
     Place x;
     x.r = warp_request_of(p.kv, token, lane);
@@ -63,14 +80,8 @@ __device__ __forceinline__ Place token_place(const AppendArgs &p, uint32_t token
     x.place = x.slot = 0;
     if (x.r >= p.kv.n_reqs) return x;
     const Request q = load_request(p.kv, x.r);
-    if (q.status != SZ_OK || q.n > q.kv || token < (uint32_t)q.q0 || token >= (uint32_t)(q.q0 + q.n)) {
-        x.r = p.kv.n_reqs;
-        return x;
-    }
-    x.place = (uint32_t)(q.kv - q.n) + (token - (uint32_t)q.q0);
-    x.slot = x.place % p.kv.page_tokens;
-    x.page = page_of(p.kv, x.r, x.place / p.kv.page_tokens);
-    if (x.page < 0) x.r = p.kv.n_reqs;
+    if (owns(q, token)) return place_in(p, x.r, q, token);
+    x.r = p.kv.n_reqs;
     return x;
 }
 
@@ -106,9 +117,10 @@ __device__ __forceinline__ uint2 narrow4(float a, float b, float c, float d) {
 __device__ __forceinline__ uint2 ld_stream_v2(const void *p) { return __ldcs(reinterpret_cast<const uint2 *>(p)); }
 
 // One token's heads [h_begin, h_end) by one warp; kLanes lanes hold one head.
+// Its request is looked up unless known (known_r < n_reqs).
 template <typename T, int kLanes, bool kAdjacent, bool kCount>
 __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token, uint32_t h_begin, uint32_t h_end, uint32_t lane,
-                                             float2 *cs, uint32_t column) {
+                                             float2 *cs, uint32_t column, uint32_t known_r, const Request &known) {
     constexpr uint32_t kHeads = 32 / kLanes;  // at a time
     const sz_paged_kv &kv = p.kv;
     const sz_append_args &a = p.a;
@@ -117,8 +129,8 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
     const bool in_head = l * 8 < D, turns_here = l < turning;
     // this lane's two runs of four channels
     const uint32_t c0 = kAdjacent ? l * 8 : turns_here ? l * 4 : l * 8;
-    const uint32_t c1 = kAdjacent || !turns_here ? c0 + 4 : c0 + pairs;
-    float cos4[4], sin4[4];
+    const uint32_t delta = kAdjacent || !turns_here ? 4 : pairs, c1 = c0 + delta;
+    float cos4[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sin4[4] = {};
     Place at;
     at.r = kv.n_reqs + 1;  // not looked up
     at.page = at.slot = at.place = 0;
@@ -131,26 +143,35 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
         if (from >= to) continue;
         const uint16_t *src = (const uint16_t *)(segment == 0 ? a.d_q_or_null : segment == 1 ? a.d_k : a.d_v);
         const uint64_t *const ss = segment == 0 ? a.q_stride : segment == 1 ? a.k_stride : a.v_stride;
-        const uint64_t src_head = ss[1];
-        src += token * ss[0] + (from + group) * src_head;
+        const uint64_t src_step = ss[1] * kHeads;
+        src += token * ss[0] + (from + group) * ss[1] + c0;
         const uint16_t *const w = (const uint16_t *)(segment == 0 ? a.d_q_norm_or_null : segment == 1 ? a.d_k_norm_or_null : nullptr);
+        const bool turn = pairs && segment < 2;
+        uint2 wu_raw = make_uint2(0, 0), wv_raw = wu_raw;
+        if (w && in_head) {
+            wu_raw = __ldg((const uint2 *)(w + c0));
+            wv_raw = __ldg((const uint2 *)(w + c1));
+        }
         uint16_t *dst = nullptr;
-        uint64_t dst_head = 0;
-        for (uint32_t h0 = from; h0 < to; h0 += kBatch * kHeads) {
+        uint64_t dst_step = 0;
+        // kBatch heads per lane; `checked`: some of them, or some lanes, may
+        // lie outside
+        auto batch = [&](uint32_t h0, auto checked) {
+            constexpr bool kChecked = decltype(checked)::value;
             uint2 x0[kBatch], x1[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                x0[i] = x1[i] = make_uint2(0, 0);
-                if (h0 + i * kHeads + group < to && in_head) {
-                    x0[i] = ld_stream_v2(src + i * (kHeads * src_head) + c0);
-                    x1[i] = ld_stream_v2(src + i * (kHeads * src_head) + c1);
+                if (!kChecked || (h0 + i * kHeads + group < to && in_head)) {
+                    x0[i] = ld_stream_v2(src);
+                    x1[i] = ld_stream_v2(src + delta);
+                } else {
+                    x0[i] = x1[i] = make_uint2(0, 0);
                 }
+                src += src_step;
             }
-            src += kBatch * kHeads * src_head;
             if (at.r > kv.n_reqs) {  // once, with loads under way
-                at = token_place(p, token, lane);
-                if (at.r >= kv.n_reqs) return;
-                if (pairs && segment < 2) {
+                at = known_r < kv.n_reqs ? place_in(p, known_r, known, token) : token_place(p, token, lane);
+                if (at.r < kv.n_reqs && turn) {
                     const double pos = a.d_positions_or_null ? (double)a.d_positions_or_null[token] : (double)at.place;
                     __syncwarp();  // the last token's angles have been read
                     for (uint32_t t = lane; t < pairs; t += 32) {
@@ -161,31 +182,31 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
                         cs[t] = make_float2(cn * a.rot_scale, sn * a.rot_scale);
                     }
                     __syncwarp();
-                }
+                    if (turns_here)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 y = pairs && segment < 2 && turns_here ? cs[l * 4 + i] : make_float2(1.0f, 0.0f);
-                    cos4[i] = y.x;
-                    sin4[i] = y.y;
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 y = cs[l * 4 + i];
+                            cos4[i] = y.x;
+                            sin4[i] = y.y;
+                        }
                 }
             }
+            if (at.r >= kv.n_reqs) return;
             if (dst == nullptr) {
                 if (segment == 0) {
-                    dst = (uint16_t *)a.d_q_out + token * a.q_out_stride[0];
-                    dst_head = a.q_out_stride[1];
+                    dst = (uint16_t *)a.d_q_out + token * a.q_out_stride[0] + (from + group) * a.q_out_stride[1] + c0;
+                    dst_step = a.q_out_stride[1] * kHeads;
                 } else {
                     const uint64_t *const ds = segment == 1 ? kv.k_stride : kv.v_stride;
-                    dst = (uint16_t *)(segment == 1 ? kv.d_k : kv.d_v) + (uint64_t)at.page * ds[0] + at.slot * ds[2];
-                    dst_head = ds[1];
+                    dst = (uint16_t *)(segment == 1 ? kv.d_k : kv.d_v) + (uint64_t)at.page * ds[0] + at.slot * ds[2] + (from + group) * ds[1] + c0;
+                    dst_step = ds[1] * kHeads;
                 }
-                dst += (from + group) * dst_head;
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (h0 + i * kHeads >= to) break;
-                const bool live = h0 + i * kHeads + group < to && in_head;
+                if (kChecked && h0 + i * kHeads >= to) break;
                 uint2 y0 = x0[i], y1 = x1[i];
-                if (w || (pairs && segment < 2)) {
+                if (w || turn) {
                     float u[4], v[4];
                     widen4<T>(y0, u);
                     widen4<T>(y1, v);
@@ -196,15 +217,13 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
 #pragma unroll
                         for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
                         const float f = rsqrtf(sum / (float)D + a.eps);
-                        float wu[4] = {}, wv[4] = {};
-                        if (in_head) {
-                            widen4<T>(__ldg((const uint2 *)(w + c0)), wu);
-                            widen4<T>(__ldg((const uint2 *)(w + c1)), wv);
-                        }
+                        float wu[4], wv[4];
+                        widen4<T>(wu_raw, wu);
+                        widen4<T>(wv_raw, wv);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) u[e] *= f * wu[e], v[e] *= f * wv[e];
                     }
-                    if (turns_here) {
+                    if (turn && turns_here) {
                         // pair i: (u[i], v[i]), or neighbours in u then v
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -218,30 +237,36 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
                     y0 = narrow4<T>(u[0], u[1], u[2], u[3]);
                     y1 = narrow4<T>(v[0], v[1], v[2], v[3]);
                 }
-                if (live) {
-                    *reinterpret_cast<uint2 *>(dst + i * (kHeads * dst_head) + c0) = y0;
-                    *reinterpret_cast<uint2 *>(dst + i * (kHeads * dst_head) + c1) = y1;
+                if (!kChecked || (h0 + i * kHeads + group < to && in_head)) {
+                    *reinterpret_cast<uint2 *>(dst) = y0;
+                    *reinterpret_cast<uint2 *>(dst + delta) = y1;
                     if (kCount && segment > 0) {
                         count2(y0, column);
                         count2(y1, column);
                     }
                 }
+                dst += dst_step;
             }
-            dst += kBatch * kHeads * dst_head;
-        }
+        };
+        uint32_t h0 = from;
+        if (D == kLanes * 8)
+            for (; h0 + kBatch * kHeads <= to; h0 += kBatch * kHeads) batch(h0, std::false_type{});
+        for (; h0 < to; h0 += kBatch * kHeads) batch(h0, std::true_type{});
+        if (at.r >= kv.n_reqs) return;
     }
 }
 
 template <typename T, int kLanes, bool kAdjacent, bool kCount>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ AppendArgs p) {
-    __shared__ float2 cs[kAppendWarps][kMaxHeadDim / 2];
+__global__ void __launch_bounds__(32 * (kCount ? kCountWarps : kAppendWarps), kCount ? 3 : 8) append_kernel(const __grid_constant__ AppendArgs p) {
+    constexpr uint32_t kWarps = kCount ? kCountWarps : kAppendWarps, kThreads = 32 * kWarps;
+    __shared__ float2 cs[kWarps][kMaxHeadDim / 2];
     __shared__ uint32_t columns[kCount ? 256 * 32 : 1];
     const sz_paged_kv &kv = p.kv;
     const uint32_t tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
     // ---- the requests' statuses: warps of the first row of blocks take one each
     if (blockIdx.y == 0) {
-        for (uint32_t r = blockIdx.x * kAppendWarps + wid; r < kv.n_reqs; r += gridDim.x * kAppendWarps) {
+        for (uint32_t r = blockIdx.x * kWarps + wid; r < kv.n_reqs; r += gridDim.x * kWarps) {
             const Request q = load_request(kv, r);
             sz_status st = q.status;
             uint32_t k_row, v_row;
@@ -258,8 +283,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
     const uint32_t all = p.a.q_heads + 2 * kv.heads;
     if constexpr (!kCount) {
         const uint32_t h_begin = blockIdx.y * p.slice_heads, h_end = umin32(all, h_begin + p.slice_heads);
-        for (uint32_t t = t_begin + wid; t < t_end; t += kAppendWarps)
-            append_token<T, kLanes, kAdjacent, false>(p, t, h_begin, h_end, lane, cs[wid], 0);
+        for (uint32_t t = t_begin + wid; t < t_end; t += kWarps)
+            append_token<T, kLanes, kAdjacent, false>(p, t, h_begin, h_end, lane, cs[wid], 0, kv.n_reqs, Request{});
     } else {
         // Block rows: keys, values and (if any) queries.  The counts of a
         // request's tokens are added to its row before the next request's.
@@ -267,7 +292,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
         const uint32_t h_begin = is_q ? 0 : p.a.q_heads + (is_v ? kv.heads : 0);
         const uint32_t h_end = is_q ? p.a.q_heads : h_begin + kv.heads;
         if (!is_q) {
-            for (uint32_t i = tid; i < 256 * 32 / 4; i += kAppendThreads) reinterpret_cast<uint4 *>(columns)[i] = make_uint4(0, 0, 0, 0);
+            for (uint32_t i = tid; i < 256 * 32 / 4; i += kThreads) reinterpret_cast<uint4 *>(columns)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
         const uint32_t column = smem_u32(columns) + 4 * lane;
@@ -276,9 +301,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
             const uint32_t r = warp_request_of(kv, t, lane);
             uint32_t stop = t_end, k_row = 0, v_row = 0;
             bool counted = false;
+            Request q{};
             if (r < kv.n_reqs) {
-                const Request q = load_request(kv, r);
-                if (q.status == SZ_OK && t >= (uint32_t)q.q0 && t < (uint32_t)(q.q0 + q.n)) {
+                q = load_request(kv, r);
+                if (owns(q, t)) {
                     stop = umin32(t_end, (uint32_t)(q.q0 + q.n));
                     counted = hist_rows(p, r, k_row, v_row);
                 } else {
@@ -286,11 +312,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
                 }
             }
             if (counted) {
-                for (uint32_t i = t + wid; i < stop; i += kAppendWarps)
+                for (uint32_t i = t + wid; i < stop; i += kWarps)
                     if (is_q)
-                        append_token<T, kLanes, kAdjacent, false>(p, i, h_begin, h_end, lane, cs[wid], 0);
+                        append_token<T, kLanes, kAdjacent, false>(p, i, h_begin, h_end, lane, cs[wid], 0, r, q);
                     else
-                        append_token<T, kLanes, kAdjacent, true>(p, i, h_begin, h_end, lane, cs[wid], column);
+                        append_token<T, kLanes, kAdjacent, true>(p, i, h_begin, h_end, lane, cs[wid], column, r, q);
                 if (!is_q) {
                     __syncthreads();
                     uint32_t sum = 0;  // thread = bin; its 32 columns from another start in every lane
@@ -315,11 +341,12 @@ static cudaError_t launch_append_lanes(AppendArgs &p, int sms, cudaStream_t s) {
     const uint64_t tokens = p.kv.n_tokens;
     if (p.a.d_hists_or_null) {
         // Counts cost a pass over 32 KB of shared memory per block and request:
-        // about four blocks per SM in all, of at least a token per warp.
-        const uint64_t want = umax64(1, (uint64_t)sms * 4 / 2);
-        p.tokens_per_block = (uint32_t)umax64(kAppendWarps, div_up(tokens, want));
+        // as many blocks as run at once (three per SM, half of them keys and
+        // half values), of at least a token per warp.
+        const uint64_t want = umax64(1, (uint64_t)sms * 3 / 2);
+        p.tokens_per_block = (uint32_t)umax64(kCountWarps, div_up(tokens, want));
         const dim3 grid((uint32_t)umax64(1, div_up(tokens, p.tokens_per_block)), p.a.q_heads ? 3 : 2);
-        append_kernel<T, kLanes, kAdjacent, true><<<grid, kAppendThreads, 0, s>>>(p);
+        append_kernel<T, kLanes, kAdjacent, true><<<grid, 32 * kCountWarps, 0, s>>>(p);
         return cudaGetLastError();
     }
     // A warp takes a token's heads in slices: as many warps as keep the SMs
@@ -329,7 +356,7 @@ static cudaError_t launch_append_lanes(AppendArgs &p, int sms, cudaStream_t s) {
     p.slice_heads = (uint32_t)umin64(groups, per_warp) * at_once;
     p.tokens_per_block = kAppendWarps;
     const dim3 grid((uint32_t)umax64(1, div_up(tokens, kAppendWarps)), (uint32_t)div_up(heads, p.slice_heads));
-    append_kernel<T, kLanes, kAdjacent, false><<<grid, kAppendThreads, 0, s>>>(p);
+    append_kernel<T, kLanes, kAdjacent, false><<<grid, 32 * kAppendWarps, 0, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -512,6 +512,65 @@ __device__ __forceinline__ void hide(uint32_t (&s)[64], int32_t from, int32_t to
         if (j < from || j >= to) s[j] = 0xFF800000u;
 }
 
+// One row's accumulator over the visible ones of keys [from, to), by one
+// warp: sum 2^(c s_j - ref) v_j.  A key hidden from a row has weight 0 in the
+// products, and 0 * inf there is NaN: a row whose accumulator holds a NaN
+// while its sum does not is computed again here from the keys it sees alone.
+// (If one of those is the reason, the loop ends when every channel is NaN.)
+// Writes the scaled 16-bit row to `out`, or the 32-bit one to `part`.
+template <typename T, int D>
+__device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32_t kv_head, const uint16_t *q, int32_t from, int32_t to,
+                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step) {
+    constexpr uint32_t kLanes = D / 8, kGroups = 32 / kLanes;  // lanes per key, keys at a time
+    const sz_paged_kv &kv = p->kv;
+    const uint32_t lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
+    float x[8], o[8] = {};
+    widen8<T>(*(const uint4 *)(q + l * 8), x);
+    for (int32_t j0 = from; j0 < to; j0 += (int32_t)kGroups) {
+        const int32_t j = j0 + (int32_t)group;
+        const int32_t page = j < to ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
+        const uint32_t slot = (uint32_t)j % kv.page_tokens;
+        float k[8] = {}, v[8] = {};
+        if (page >= 0) {
+            widen8<T>(*(const uint4 *)((const uint16_t *)kv.d_k + (uint64_t)page * kv.k_stride[0] + kv_head * kv.k_stride[1] +
+                                       slot * kv.k_stride[2] + l * 8), k);
+            widen8<T>(*(const uint4 *)((const uint16_t *)kv.d_v + (uint64_t)page * kv.v_stride[0] + kv_head * kv.v_stride[1] +
+                                       slot * kv.v_stride[2] + l * 8), v);
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[i] * k[i];
+#pragma unroll
+        for (int d = kLanes / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        bool gone = true;
+        if (page >= 0) {
+            const float w = exp2f(fmaf(s, p->c, -ref));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] += w * v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gone &= o[i] != o[i];
+        const uint32_t all = __ballot_sync(0xFFFFFFFFu, gone);
+        bool end = false;
+#pragma unroll
+        for (uint32_t g = 0; g < kGroups; ++g) end |= (all >> (g * kLanes) & ((1ull << kLanes) - 1)) == (1ull << kLanes) - 1;
+        if (end) break;
+    }
+#pragma unroll
+    for (uint32_t d = kLanes; d < 32; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xFFFFFFFFu, o[i], d);
+    if (group != 0) return;
+    if (out) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] *= inv;
+        *(uint4 *)(out + l * 8) = narrow8<T>(o);
+    } else {
+        *(float4 *)(part + (2 * l) * part_step) = make_float4(o[0], o[1], o[2], o[3]);
+        *(float4 *)(part + (2 * l + 1) * part_step) = make_float4(o[4], o[5], o[6], o[7]);
+    }
+}
+
 struct Bars {
     uint64_t full[10], empty[10];
     uint64_t q_full[2], q_empty[2];
@@ -934,14 +993,39 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             const float2 both = unpack2(sum);
             const float l = both.x + both.y;
             tc_fence_after();
-            const bool mine = row < rows;
+            if (!warp_live) continue;
+            bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
             const float ref = m * p.c;  // log2 units
-            if (w.starts && w.ends) {
-                if (!warp_live) continue;
-                const bool any = begin < stop;
-                const float inv = any ? 1.0f / l : 0.0f;
-                uint16_t *out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
+            const bool whole = w.starts && w.ends, any = begin < stop;
+            const float inv = any ? 1.0f / l : 0.0f;
+            uint16_t *const out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];
+            float *const part = p.parts + (size_t)(blockIdx.x * 2 + (w.starts ? 1 : 0)) * S::kPartFloats;
+            // a NaN that the sum does not have: from a hidden key's values?
+            uint64_t seen = pack2(0.0f, 0.0f);
+#pragma unroll 1
+            for (uint32_t i = 0; i < D / 32; ++i) {
+                uint32_t o[32];
+                tmem_ld32(o_at + i * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) seen = add2(seen, pack2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])));
+            }
+            const float2 seen2 = unpack2(seen);
+            uint32_t odd = __ballot_sync(0xFFFFFFFFu, mine && seen2.x + seen2.y != seen2.x + seen2.y && l > 0.0f && *fail == 0);
+            if (odd >> lane & 1u) mine = false;
+            while (odd) {
+                const int src = __ffs(odd) - 1;
+                odd &= odd - 1;
+                const uint32_t t = __shfl_sync(0xFFFFFFFFu, token, src), h = __shfl_sync(0xFFFFFFFFu, head, src);
+                const int32_t from = max(__shfl_sync(0xFFFFFFFFu, begin, src), w.t0 * (int32_t)p.key_tile);
+                const int32_t to = min(__shfl_sync(0xFFFFFFFFu, stop, src), w.t1 * (int32_t)p.key_tile);
+                const float ref1 = __shfl_sync(0xFFFFFFFFu, ref, src), inv1 = __shfl_sync(0xFFFFFFFFu, inv, src);
+                uint16_t *const out1 = whole ? (uint16_t *)p.a.d_out + (uint64_t)t * p.a.out_stride[0] + (uint64_t)h * p.a.out_stride[1] : nullptr;
+                visible_row<T, D>(&p, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)t * p.a.q_stride[0] + (uint64_t)h * p.a.q_stride[1], from, to,
+                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0));
+            }
+            if (whole) {
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
@@ -955,23 +1039,20 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         if (mine) *(uint4 *)(out + i * 32 + j * 8) = narrow8<T>(x);
                     }
                 }
-                if (mine && p.a.d_lse_or_null)
+                if (row < rows && p.a.d_lse_or_null)
                     p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any ? (l > 0.0f || l != l ? (ref + log2f(l)) * kLn2 : -INFINITY) : -INFINITY;
             } else {
-                float *part = p.parts + (size_t)(blockIdx.x * 2 + (w.starts ? 1 : 0)) * S::kPartFloats;
-                if (warp_live) {
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + i * 32, o);
-                        tmem_wait_ld();
-                        if (mine)
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + i * 32, o);
+                    tmem_wait_ld();
+                    if (mine)
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *(uint4 *)(part + S::part_o(m_tile, i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                    }
-                    if (mine) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
+                        for (int j = 0; j < 8; ++j)
+                            *(uint4 *)(part + S::part_o(m_tile, i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
+                if (row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
             }
         }
         tc_fence_before();

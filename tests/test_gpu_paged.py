@@ -168,6 +168,58 @@ def test_infinite_and_nan_scores(dim):
     assert bool(torch.isinf(out[3, :, 1]).all()) and bool(torch.isfinite(out[3, :, 2:]).all())
 
 
+@pytest.mark.parametrize("shape", [([5], [40], 4, 2, 128), ([200], [200], 4, 1, 128), ([150], [290], 2, 2, 64), ([2, 1], [9000, 60], 4, 1, 64),
+                                   ([9], [30], 2, 1, 72)], ids=str)
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_values_hidden_from_a_row_do_not_reach_it(shape, value):
+    # the last token's value is not finite: the rows before it do not see it;
+    # with a window, nor do rows past the first key's
+    new, kv, hq, hk, dim = shape
+    for window in (0, 33):
+        b = Batch(new, kv, hq, hk, dim, 16, BF16)
+        k, v, table, q_begin, kv_len = b.cache()
+        last, early = kv[0] - 1, max(0, kv[0] - new[0] - 20)
+        want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim), True, window)
+        v[int(b.table[0, last // 16]), :, last % 16, 3::5] = value
+        if window:
+            v[int(b.table[0, early // 16]), :, early % 16, 1] = value
+        out, lse, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, window=window, return_lse=True)
+        assert not status.any()
+        out = out.cpu()
+        # rows of request 0 that see neither key; all of the others
+        p = torch.arange(kv[0] - new[0], kv[0])
+        clean = p < last
+        if window:
+            clean &= (p < early) | (p - window >= early)
+        clean = torch.cat((clean, torch.ones(b.rows - new[0], dtype=torch.bool)))
+        check(out[clean], want[0][clean], want[2][clean])
+        check(lse, want[1], want[3])
+        assert not torch.isfinite(out[new[0] - 1, :, 3::5].float()).any()
+        same = torch.ones(dim, dtype=torch.bool)
+        same[3::5] = False
+        check(out[new[0] - 1, :, same], want[0][new[0] - 1, :, same], want[2][new[0] - 1, :, same]) if not window else None
+
+
+def test_waits_that_run_out_are_reported():
+    # the copy warps issue nothing, so every wait ends by its limit
+    few, many = Batch([1, 2], [3000, 70], 8, 2, 128, 16, BF16), Batch([300], [900], 8, 2, 64, 16, FP16)
+    ws = torch.empty(sz.sz_plan_attention(128), dtype=torch.uint8, device=DEV)
+    for b in (few, many):
+        args = [b.q.to(DEV)] + b.cache()
+        good = sz.paged_attention(*args, workspace=ws)[0].clone()
+        try:
+            sz.sz_debug_set_flags(1)
+            sz.sz_set_wait_limit_ns(2_000_000)
+            _, _, status = sz.paged_attention(*args, workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            sz.sz_debug_set_flags(0)
+            sz.sz_set_wait_limit_ns(1_000_000_000)
+        assert status.cpu().tolist() == [sz.SZ_ERR_DEVICE_TIMEOUT] * len(b.kv)
+        again, _, status = sz.paged_attention(*args, workspace=ws)
+        assert not status.any() and torch.equal(again, good)
+
+
 @pytest.mark.parametrize("layout", ["token_major", "one_pool", "rows_of_a_projection", "in_place"])
 @pytest.mark.parametrize("dim", [128, 40])
 def test_attention_layouts(layout, dim):
