@@ -161,8 +161,6 @@ constexpr int kPolyEvery = SZ_POLY;  // every so many pairs of weights take the 
 constexpr uint32_t kWholeTiles = 6;                     // blocks up to this long are not split when there is a CTA for each
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
-constexpr uint32_t kControlBytes = 768;                // of shared memory: barriers and the CTA's share
-
 template <int D, int kM>
 struct Shape {
     static constexpr int kTiles = kM, kHalves = D / 64;
@@ -174,12 +172,19 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
     static constexpr int kQueries = D == 64 ? 2 : 1;  // blocks whose queries are in shared memory at a time
     static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6);
-    static constexpr int kSoftmaxWarps = kRows / 32, kSoftmaxThreads = kM * kSoftmaxWarps * 32;  // warps per row tile
-    static constexpr int kThreads = kSoftmaxThreads + 128;
+    // Warps.  A softmax warp holds 32 rows and half of a key tile's columns;
+    // which lanes of tensor memory it reaches goes by its number modulo 4.
+    //   kM = 2: 0..15 softmax (row tile, half, 32 rows), 16, 17 products, 18 copies of Q and K, 19 of V
+    //   kM = 1: 0, 1 and 4, 5 softmax, 2 products, 3 and 6 copies, 7 statuses
+    static constexpr uint32_t kQuads = kRows / 32;  // warps per half of a row tile
+    static constexpr uint32_t kMmaWarp = kM == 2 ? 16 : 2, kKeyWarp = kM == 2 ? 18 : 3, kValueWarp = kM == 2 ? 19 : 6;
+    static constexpr uint32_t kStatusWarp = kM == 2 ? kValueWarp : 7;
+    static constexpr int kThreads = kM == 2 ? 640 : 256;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
     static constexpr uint32_t kQueryHalf = kRows * kRowBytes, kQueryTile = kHalves * kQueryHalf, kQueryBytes = kM * kQueryTile;
     static constexpr uint32_t kData = kQueries * kQueryBytes + kSlots * kTileBytes;
+    static constexpr uint32_t kControlBytes = 384 + 2 * 4 * kM * kRows;  // barriers, the CTA's share, exchanged numbers
     static constexpr uint32_t kSmem = kData + kControlBytes;
     // A part of a block: per row tile 4 channels of all rows, the next 4, ...
     // (so that threads that hold a row each write and read side by side),
@@ -360,8 +365,6 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
 }
 
 struct PlanShared {
-    uint64_t warp_units[12], warp_blocks[12];
-    uint32_t warp_most[12];
     uint64_t total;
     uint64_t first, left;  // this CTA's units
     uint32_t used;         // CTAs with work
@@ -370,9 +373,15 @@ struct PlanShared {
     Request q;
 };
 
+// What the search for it exchanges between warps.
+struct PlanScratch {
+    uint64_t units[20], blocks[20];
+    uint32_t most[20];
+};
+
 // This CTA's share of the units, found by all of its threads.
 template <int kM, int kThreads>
-__device__ void find_share(const TensorArgs &p, PlanShared &s) {
+__device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
     constexpr uint32_t kW = kThreads / 32;
     const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const uint32_t rounds = (p.kv.n_reqs + 32 * kW - 1) / (32 * kW);
@@ -388,17 +397,17 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
     blocks = warp_sum(blocks) * p.kv.heads;
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     if (lane == 0) {
-        s.warp_units[wid] = mine;
-        s.warp_blocks[wid] = blocks;
-        s.warp_most[wid] = most;
+        x.units[wid] = mine;
+        x.blocks[wid] = blocks;
+        x.most[wid] = most;
     }
     __syncthreads();
     uint64_t total = 0, before = 0, total_blocks = 0, before_blocks = 0;
     for (uint32_t w = 0; w < kW; ++w) {
-        if (w < wid) before += s.warp_units[w], before_blocks += s.warp_blocks[w];
-        total += s.warp_units[w];
-        total_blocks += s.warp_blocks[w];
-        most = max(most, s.warp_most[w]);
+        if (w < wid) before += x.units[w], before_blocks += x.blocks[w];
+        total += x.units[w];
+        total_blocks += x.blocks[w];
+        most = max(most, x.most[w]);
     }
     // A few short blocks: one CTA each, which costs less than joining parts.
     const bool whole = total_blocks <= p.ctas && most <= kWholeTiles;
@@ -433,16 +442,16 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
             rem -= __shfl_sync(0xFFFFFFFFu, end - units * p.kv.heads, src);
             const uint32_t head = (uint32_t)divide(rem, w);
             rem -= head * w;
-            Request x;
-            x.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, src);
-            x.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
-            x.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
-            x.status = SZ_OK;
-            for (uint32_t b0 = 0; b0 < block_count<kM>(p, x); b0 += 32) {
+            Request own;
+            own.q0 = __shfl_sync(0xFFFFFFFFu, q.q0, src);
+            own.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
+            own.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
+            own.status = SZ_OK;
+            for (uint32_t b0 = 0; b0 < block_count<kM>(p, own); b0 += 32) {
                 uint64_t n = 0;
-                if (b0 + lane < block_count<kM>(p, x)) {
+                if (b0 + lane < block_count<kM>(p, own)) {
                     int32_t lo, hi;
-                    block_tiles<kM>(p, x, b0 + lane, &lo, &hi);
+                    block_tiles<kM>(p, own, b0 + lane, &lo, &hi);
                     n = whole ? 1u : (uint32_t)(hi - lo) + kBlockUnits<kM>;
                 }
                 const uint64_t stop = warp_scan(n, lane);
@@ -458,7 +467,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s) {
                     s.head = head;
                     s.block = b0 + (uint32_t)at;
                     s.off = (uint32_t)rem;
-                    s.q = x;
+                    s.q = own;
                     s.left = u1 - u0;
                 }
                 break;
@@ -505,11 +514,26 @@ __device__ __forceinline__ void wait_or_fail(uint64_t *bar, uint32_t parity, vol
     }
 }
 
-// Columns outside [from, to) of 64 scores become -inf.
-__device__ __forceinline__ void hide(uint32_t (&s)[64], int32_t from, int32_t to) {
+// Columns outside [from, to) of a row's scores become -inf.
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&s)[N], int32_t from, int32_t to) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
+    for (int j = 0; j < N; ++j)
         if (j < from || j >= to) s[j] = 0xFF800000u;
+}
+
+// Barriers of the two warps that hold the same rows; one also tells whether
+// any of their threads has `x`.
+__device__ __forceinline__ void pair_sync(uint32_t id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(uint32_t id, bool x) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(x ? 1u : 0u)
+        : "memory");
+    return any != 0;
 }
 
 // One row's accumulator over the visible ones of keys [from, to), by one
@@ -517,10 +541,11 @@ __device__ __forceinline__ void hide(uint32_t (&s)[64], int32_t from, int32_t to
 // products, and 0 * inf there is NaN: a row whose accumulator holds a NaN
 // while its sum does not is computed again here from the keys it sees alone.
 // (If one of those is the reason, the loop ends when every channel is NaN.)
-// Writes the scaled 16-bit row to `out`, or the 32-bit one to `part`.
+// Writes half of the channels of the scaled 16-bit row to `out`, or of the
+// 32-bit one to `part`.
 template <typename T, int D>
 __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32_t kv_head, const uint16_t *q, int32_t from, int32_t to,
-                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step) {
+                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t half) {
     constexpr uint32_t kLanes = D / 8, kGroups = 32 / kLanes;  // lanes per key, keys at a time
     const sz_paged_kv &kv = p->kv;
     const uint32_t lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
@@ -560,7 +585,7 @@ __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32
     for (uint32_t d = kLanes; d < 32; d <<= 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xFFFFFFFFu, o[i], d);
-    if (group != 0) return;
+    if (group != 0 || l / (kLanes / 2) != half) return;
     if (out) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= inv;
@@ -575,15 +600,19 @@ struct Bars {
     uint64_t full[10], empty[10];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], pv_done[2];
-    uint64_t drain;
+    uint64_t drain[2];
 };
 
+template <int D, int kM>
 struct Control {  // behind the tiles in shared memory
     Bars bars;
     PlanShared plan;
     uint32_t tmem, failed;
+    union {
+        PlanScratch scratch;
+        float swap[2][kM * Shape<D, kM>::kRows];  // between the two halves of a row: maxima, sums
+    };
 };
-static_assert(sizeof(Control) <= kControlBytes, "control block");
 
 template <typename T, int D, int kM>
 __global__ void __launch_bounds__(Shape<D, kM>::kThreads, Shape<D, kM>::kCtasPerSm)
@@ -594,6 +623,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     constexpr uint32_t kScoreWord = mma_word(kBf16, 128, false);
     constexpr uint32_t kOutWord = mma_word(kBf16, D, true);
     extern __shared__ __align__(1024) uint8_t raw[];
+    using Control = Control<D, kM>;
+    static_assert(sizeof(Control) <= S::kControlBytes, "control block");
     Control &control = *reinterpret_cast<Control *>(raw + S::kData);
     Bars &bars = control.bars;
     PlanShared &plan = control.plan;
@@ -604,29 +635,31 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint32_t tid = threadIdx.x, wid = same(tid >> 5), lane = tid & 31;
     const uint32_t smem0 = smem_u32(raw);
     const uint32_t ring0 = smem0 + S::kQueries * S::kQueryBytes;
-    constexpr uint32_t kMmaWarp = kM * S::kSoftmaxWarps, kCopyWarp = kMmaWarp + 1, kStatusWarp = kMmaWarp + 3;
+    constexpr uint32_t kMmaWarp = S::kMmaWarp;
+    const bool softmax = kM == 2 ? wid < 16 : (wid & 3) < 2 && wid < 6;
 
     if (wid == kMmaWarp) tmem_alloc(&control.tmem, S::kColumns);
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], 1);
+            mbar_init(&bars.empty[i], kM);
         }
         for (int i = 0; i < S::kQueries; ++i) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], 1);
+            mbar_init(&bars.q_empty[i], kM);
         }
         for (int x = 0; x < kM; ++x) {
             mbar_init(&bars.s_full[x], 1);
-            mbar_init(&bars.p_full[x][0], S::kSoftmaxWarps);
-            mbar_init(&bars.p_full[x][1], S::kSoftmaxWarps);
+            mbar_init(&bars.p_full[x][0], S::kQuads);
+            mbar_init(&bars.p_full[x][1], S::kQuads);
             mbar_init(&bars.pv_done[x], 1);
         }
-        mbar_init(&bars.drain, 1);
+        mbar_init(&bars.drain[0], 1);
+        mbar_init(&bars.drain[1], 1);
         fence_mbar_init();
         failed = 0;
     }
-    if (wid == kCopyWarp && lane == 0) {
+    if (wid == S::kKeyWarp && lane == 0) {
         prefetch_map(&q_map);
         prefetch_map(&k_map);
         prefetch_map(&v_map);
@@ -639,7 +672,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring0 + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0) : "memory");
         }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    find_share<kM, S::kThreads>(p, plan);  // synchronises the block
+    find_share<kM, S::kThreads>(p, plan, control.scratch);  // synchronises the block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -656,27 +689,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     volatile uint32_t *const fail = &failed;
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
-    if (wid >= kMmaWarp) {
-        if (wid == kStatusWarp) {
-        // ---------------------------------------------------------- statuses
-        for (uint32_t r = blockIdx.x; r < p.kv.n_reqs; r += gridDim.x) {
-            const Request q = load_request(p.kv, r);
-            sz_status st = q.status;
-            if (st == SZ_OK && q.n > 0 && q.kv > 0) {
-                int32_t begin, stop;
-                key_range(p, q, 0, q.n, &begin, &stop);
-                st = check_pages(p.kv, r, (uint32_t)begin / p.kv.page_tokens, (uint32_t)(q.kv - 1) / p.kv.page_tokens + 1);
-            }
-            if (lane == 0) {
-                p.status[r] = st;
-                __threadfence();  // a CTA that fails sets timed_out, then the statuses
-                if (*(volatile unsigned long long *)p.timed_out == p.call) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
-            }
-        }
-        } else if (wid >= kCopyWarp) {
+    if (!softmax) {
+        if (wid == S::kKeyWarp || wid == S::kValueWarp) {
         // ------------------------------------- copies: Q and K, or V
         const bool one = elect_one();
-        const uint32_t is_v = wid - kCopyWarp;
+        const uint32_t is_v = wid == S::kValueWarp ? 1u : 0u;
         const CUtensorMap *const map = is_v ? &v_map : &k_map;
         const bool silent = (p.debug_flags & kDebugNoSignal) != 0;
         const uint32_t tile_bytes = p.key_tile * S::kHalves * kRowBytes;
@@ -756,134 +773,94 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             for (uint32_t u = pieces > S::kQueries ? pieces - S::kQueries : 0; u < pieces; ++u)
                 mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, limit);
         }
-        } else if (wid == kMmaWarp) {
+        } else if (wid >= kMmaWarp && wid < kMmaWarp + kM) {
         // ---------------------------------------------------------- products
+        // One warp per row tile: issuing waits for the tensor cores' queue, and
+        // what a warp does between its products then costs the other's nothing.
         const bool one = elect_one();
-        uint32_t done[2] = {0, 0};  // score products per row tile
-        const uint32_t q_lo = desc_lo(smem0, 16), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
-        // tiles of the piece at hand: first, end, cached tokens, row tiles in use
-        int32_t t = 0, t_end = 0, kv = 0;
-        uint32_t tiles = 0;
-        auto take = [&](int32_t &a, int32_t &b, int32_t &c, uint32_t &m) -> bool {
-            const bool have = next_piece<kM>(p, cur, w);
-            a = (int32_t)same((uint32_t)w.t0);
-            b = (int32_t)same((uint32_t)w.t1);
-            c = (int32_t)same((uint32_t)w.q.kv);
-            m = same((kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens) ? 1u : 2u);
-            return same(have ? 1u : 0u) != 0;
+        const uint32_t m = wid - kMmaWarp;
+        const uint32_t q_lo = desc_lo(smem0, 16) + m * (S::kQueryTile >> 4), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
+        const uint32_t s_at = tmem + m * 128, o_at = tmem + kM * 128 + m * D;
+        uint64_t *const s_full = &bars.s_full[m], *const p_full = bars.p_full[m], *const pv_done = &bars.pv_done[m];
+        uint32_t done = 0;  // key tiles of this row tile
+        uint32_t slot = 0, phase = 0;  // of the ring, at the next K or V
+        auto pass = [&] {  // to the next of the ring
+            if (++slot == S::kSlots) slot = 0, phase ^= 1;
         };
-        auto score = [&](uint32_t m, uint32_t at, uint32_t buf) {  // S_m = Q_m K^T
-            const uint32_t a = q_lo + buf * (S::kQueryBytes >> 4) + m * (S::kQueryTile >> 4), b = k_lo + at * (S::kTileBytes >> 4);
-            if (one) {
+        for (uint32_t piece = 0; same(*fail) == 0; ++piece) {
+            if (same(next_piece<kM>(p, cur, w) ? 1u : 0u) == 0) break;
+            const int32_t t_begin = (int32_t)same((uint32_t)w.t0), t_end = (int32_t)same((uint32_t)w.t1), kv = (int32_t)same((uint32_t)w.q.kv);
+            const bool active = m == 0 || same((uint32_t)w.q.n - w.block * kM * p.tile_tokens > p.tile_tokens ? 1u : 0u) != 0;
+            const uint32_t buf = piece % S::kQueries;
+            const uint32_t qa = q_lo + buf * (S::kQueryBytes >> 4);
+            auto score = [&] {  // S = Q K^T, K at `slot`
+                const uint32_t b = k_lo + slot * (S::kTileBytes >> 4);
+                if (one) {
+                    if (active) {
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t half = (uint32_t)(i / 4), off = (uint32_t)(i % 4) * 32 >> 4;
-                    mma_smem(tmem + m * 128, full_desc(a + half * (S::kQueryHalf >> 4) + off), full_desc(b + half * (kHalfBytes >> 4) + off), kScoreWord, i > 0);
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t half = (uint32_t)(i / 4), off = (uint32_t)(i % 4) * 32 >> 4;
+                            mma_smem(s_at, full_desc(qa + half * (S::kQueryHalf >> 4) + off), full_desc(b + half * (kHalfBytes >> 4) + off), kScoreWord, i > 0);
+                        }
+                        mma_commit(s_full);
+                    }
+                    mma_commit(&bars.empty[slot]);
                 }
-                mma_commit(&bars.s_full[m]);
-            }
-            __syncwarp();
-            ++done[m];
-        };
-        bool have = take(t, t_end, kv, tiles);
-        bool first = true;  // the piece's first tile
-        uint32_t pieces = 0;                         // index of the piece at hand
-        uint32_t slot = 1 % S::kSlots, phase = 0;  // of the ring, at this tile's V
-        if (have) {
-            wait_or_fail(&bars.q_full[0], 0, fail, limit);
-            wait_or_fail(&bars.full[0], 0, fail, limit);
-            tc_fence_after();
-#pragma unroll
-            for (uint32_t m = 0; m < kM; ++m)
-                if (m < tiles) score(m, 0, 0);
-            if (one) {
-                mma_commit(&bars.empty[0]);
-                if (t + 1 == t_end) mma_commit(&bars.q_empty[0]);
-            }
-        }
-        while (have && same(*fail) == 0) {
-            int32_t nt = t + 1, nt_end = t_end, nkv = kv;
-            uint32_t ntiles = tiles;
-            bool more = true, nfirst = false;
-            if (nt >= t_end) {
-                more = take(nt, nt_end, nkv, ntiles);
-                nfirst = true;
-                ++pieces;
-                if (!more) ntiles = 0;
-            }
-            const uint32_t buf = pieces % S::kQueries;
-            // V of this tile and K of the next first, so that nothing is waited
-            // for between the weights and the products; but a next piece's Q and
-            // K may be some way off, and this piece's last products go ahead
-            const uint32_t v_slot = slot, k_slot = slot + 1 == S::kSlots ? 0 : slot + 1;
-            const uint32_t v_phase = phase, k_phase = phase ^ (k_slot == 0 ? 1u : 0u);
-            slot = k_slot + 1 == S::kSlots ? 0 : k_slot + 1;
-            phase = k_phase ^ (slot == 0 ? 1u : 0u);
-            wait_or_fail(&bars.full[v_slot], v_phase, fail, limit);
-            // keys behind the last token in this tile's last page: their
-            // weights are 0, so their values must be finite
-            const int32_t z0 = kv - t * (int32_t)p.key_tile;
-            if (z0 > 0 && z0 < (int32_t)p.key_tile) {
-                const int32_t page = (int32_t)p.kv.page_tokens;
-                const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
-                const uint32_t vb = ring0 + v_slot * S::kTileBytes;
-                for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
-                    const uint32_t piece = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0)
-                                 : "memory");
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-            }
-            if (more && !nfirst) wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
-            const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
-#pragma unroll
-            for (uint32_t m = 0; m < kM; ++m) {
-                if (m < tiles) {
+                pass();
+            };
+            wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, fail, limit);
+            wait_or_fail(&bars.full[slot], phase, fail, limit);
+            tc_fence_after();
+            score();
+            for (int32_t t = t_begin; t < t_end; ++t) {
+                const uint32_t v_slot = slot;
+                wait_or_fail(&bars.full[slot], phase, fail, limit);
+                pass();
+                if (t + 1 < t_end)  // the next K now, so that nothing is waited for between the products
+                    wait_or_fail(&bars.full[slot], phase, fail, limit);
+                else if (one)
+                    mma_commit(&bars.q_empty[buf]);
+                if (active) {
+                    // keys behind the last token in this tile's last page: their
+                    // weights are 0, so their values must be finite
+                    const int32_t z0 = kv - t * (int32_t)p.key_tile;
+                    if (z0 > 0 && z0 < (int32_t)p.key_tile) {
+                        const int32_t page = (int32_t)p.kv.page_tokens;
+                        const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
+                        const uint32_t vb = ring0 + v_slot * S::kTileBytes;
+                        for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
+                            const uint32_t chunk = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + chunk * 16), "r"(0)
+                                         : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
 #pragma unroll
                     for (uint32_t part = 0; part < 2; ++part) {  // the weights of 64 keys each
-                        wait_or_fail(&bars.p_full[m][part], (done[m] - 1) & 1, fail, limit);
+                        wait_or_fail(&p_full[part], done & 1, fail, limit);
                         tc_fence_after();
                         if (one) {
 #pragma unroll
-                            for (uint32_t k = 0; k < kTileRows / 32; ++k) {
-                                const uint32_t i = part * (kTileRows / 32) + k;
-                                mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + i * 8, full_desc(vb + i * (16 * kRowBytes >> 4)), kOutWord,
-                                         (!first || i > 0) ? 1u : 0u);
-                            }
-                            if (part == 1) mma_commit(&bars.pv_done[m]);
+                            for (uint32_t i = 0; i < 4; ++i)
+                                mma_tmem(o_at, s_at + part * 64 + i * 8, full_desc(vb + (part * 4 + i) * (16 * kRowBytes >> 4)), kOutWord,
+                                         (t > t_begin || part + i > 0) ? 1u : 0u);
+                            if (part == 1) mma_commit(pv_done);
                         }
                         __syncwarp();
                     }
+                    ++done;
                 }
-                if (m < ntiles && !nfirst) score(m, k_slot, buf);
+                if (one) mma_commit(&bars.empty[v_slot]);
+                if (t + 1 < t_end) score();
             }
-            if (more && nfirst) {
-                wait_or_fail(&bars.q_full[buf], pieces / S::kQueries & 1, fail, limit);
-                wait_or_fail(&bars.full[k_slot], k_phase, fail, limit);
-                tc_fence_after();
-#pragma unroll
-                for (uint32_t m = 0; m < kM; ++m)
-                    if (m < ntiles) score(m, k_slot, buf);
-            }
-            if (one) {
-                mma_commit(&bars.empty[v_slot]);
-                if (more) {
-                    mma_commit(&bars.empty[k_slot]);
-                    if (nt + 1 == nt_end) mma_commit(&bars.q_empty[buf]);
-                }
-            }
-            t = nt;
-            t_end = nt_end;
-            kv = nkv;
-            tiles = ntiles;
-            have = more;
-            first = nfirst;
         }
         if (*fail) {  // products under way must end before their memory is given back
             if (one) {
-                mma_commit(&bars.drain);
-                mbar_wait(&bars.drain, 0, limit);
+                mma_commit(&bars.drain[m]);
+                mbar_wait(&bars.drain[m], 0, limit);
             }
             __syncwarp();
         }
@@ -891,11 +868,13 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     } else {
         // ----------------------------------------------------------- softmax
 
-        const uint32_t m_tile = wid / S::kSoftmaxWarps;
-        const uint32_t row = tid % S::kRows;
-        const uint32_t lanes = wid % S::kSoftmaxWarps * 32;  // this warp's lanes of tensor memory
-        const uint32_t s_at = tmem + (lanes << 16) + m_tile * 128;
-        const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D;
+        const uint32_t m_tile = kM == 2 ? wid / 8 : 0, half = wid / 4 & 1, quad = wid & 3;
+        const uint32_t row = quad * 32 + lane;
+        const uint32_t lanes = quad * 32;  // of tensor memory
+        const uint32_t pair = 1 + m_tile * 4 + quad;  // barrier of the two warps that share rows
+        const uint32_t s_at = tmem + (lanes << 16) + m_tile * 128 + half * 64;
+        const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D + half * (D / 2);  // this warp's half of the channels
+        float *const swap_mine = &control.swap[half][m_tile * S::kRows + row], *const swap_other = &control.swap[half ^ 1][m_tile * S::kRows + row];
         const uint32_t my_token = row / p.group, my_head = row % p.group;
         uint32_t n = 0;  // tiles done by this row tile
         while (next_piece<kM>(p, cur, w)) {
@@ -906,68 +885,73 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             int32_t begin, stop;
             key_range(p, w.q, (int32_t)(first + my_token), (int32_t)(first + my_token) + 1, &begin, &stop);
             float m = -INFINITY;             // reference of the weights
-            uint64_t sum = pack2(0.0f, 0.0f);  // of the weights, in two parts
-            int32_t k0 = w.t0 * (int32_t)p.key_tile;
-            for (int32_t t = w.t0; t < w.t1; ++t, ++n, k0 += (int32_t)p.key_tile) {
+            uint64_t sum = pack2(0.0f, 0.0f);  // of this half's weights, in two parts
+            for (int32_t t = w.t0; t < w.t1; ++t, ++n) {
                 wait_or_fail(&bars.s_full[m_tile], n & 1, fail, limit);
                 tc_fence_after();
-                // this row's visible columns; the same for all rows of most tiles
-                const int32_t from = begin - k0, to = min(stop - k0, (int32_t)p.key_tile);
-                const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kTileRows) != 0;
-                float high = -INFINITY;
                 if (warp_live) {
-#pragma unroll 1
-                    for (uint32_t half = 0; half < 2; ++half) {
+                    // this row's visible columns; all of them in most tiles
+                    const int32_t k0 = t * (int32_t)p.key_tile + (int32_t)half * 64;
+                    const int32_t from = begin - k0, to = min(stop - k0, (int32_t)p.key_tile - (int32_t)half * 64);
+                    const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < 64) != 0;
+                    float high;
+                    {
                         uint32_t s[64];
-                        tmem_ld64(s_at + half * 64, s);
+                        tmem_ld64(s_at, s);
                         tmem_wait_ld();
-                        if (masked) hide(s, from - (int32_t)half * 64, to - (int32_t)half * 64);
-                        float top[4] = {high, -INFINITY, -INFINITY, -INFINITY};
+                        if (masked) hide(s, from, to);
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int j = 0; j < 64; j += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]));
                         high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
                     }
-                    if (t == w.t0) {
-                        m = high;
-                    } else {
-                        const bool rise = (high - m) * p.c > kRescaleAt;
-                        if (__any_sync(0xFFFFFFFFu, rise)) {
+                    // Both halves of a row use one reference: it moves when
+                    // either asks, which is at first and then rarely.
+                    const bool begins = t == w.t0;
+                    if (begins || pair_any(pair, (high - m) * p.c > kRescaleAt)) {
+                        *swap_mine = high;
+                        pair_sync(pair);
+                        high = fmaxf(high, *swap_other);
+                        if (begins) {
+                            m = high;
+                        } else {
                             // the accumulator as of the tile before
                             wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
                             tc_fence_after();
+                            const bool rise = (high - m) * p.c > kRescaleAt;
                             const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
                             if (rise) m = high;
                             sum = mul2(sum, pack2(f, f));
 #pragma unroll 1
                             for (uint32_t i = 0; i < D / 32; ++i) {
-                                uint32_t o[32];
-                                tmem_ld32(o_at + i * 32, o);
+                                uint32_t o[16];
+                                tmem_ld16(o_at + i * 16, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st32(o_at + i * 32, o);
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st16(o_at + i * 16, o);
                             }
                             tmem_wait_st();
+                            tc_fence_before();
+                            pair_sync(pair);  // the other half's channels too, before any weight is handed over
                         }
                     }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m * p.c;
-                const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
+                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
+                    const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
+                    uint64_t sum1 = pack2(0.0f, 0.0f);
+                    // The scores are read again: tensor memory is close by, and
+                    // fewer registers let more warps work.  Weights of columns
+                    // 32 i .. take columns 16 i .. of the half.
 #pragma unroll 1
-                for (uint32_t half = 0; half < 2; ++half) {
-                    if (warp_live) {
-                        // The scores are read again: tensor memory is close by,
-                        // and a row kept in registers costs more than that.
-                        // Weights of columns 64h .. take columns 32h ..
-                        uint32_t s[64];
-                        tmem_ld64(s_at + half * 64, s);
+                    for (uint32_t i = 0; i < 2; ++i) {
+                        uint32_t s[32], w16[16];
+                        tmem_ld32(s_at + i * 32, s);
                         tmem_wait_ld();
-                        if (masked) hide(s, from - (int32_t)half * 64, to - (int32_t)half * 64);
-                        uint64_t sum1 = pack2(0.0f, 0.0f);
+                        if (masked) hide(s, from - (int32_t)i * 32, to - (int32_t)i * 32);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < 16; ++j) {
                             const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, ref2);
                             uint64_t e;
                             if (j % kPolyEvery == kPolyEvery - 1) {
@@ -978,22 +962,25 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             }
                             if (j & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
                             const float2 f = unpack2(e);
-                            s[j] = Half2<T>::narrow(f.x, f.y);
+                            w16[j] = Half2<T>::narrow(f.x, f.y);
                         }
-                        sum = add2(sum, sum1);
-                        tmem_st32(s_at + half * 32, s);
-                        tmem_wait_st();
+                        tmem_st16(s_at + i * 16, w16);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.p_full[m_tile][half]);
+                    sum = add2(sum, sum1);
+                    tmem_wait_st();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[m_tile][half]);
             }
             wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
-            const float2 both = unpack2(sum);
-            const float l = both.x + both.y;
             tc_fence_after();
             if (!warp_live) continue;
+            const float2 both = unpack2(sum);
+            *swap_mine = both.x + both.y;
+            pair_sync(pair);
+            const float l = half ? *swap_other + *swap_mine : *swap_mine + *swap_other;
+            pair_sync(pair);  // read by both before it is written again
             bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
             const float ref = m * p.c;  // log2 units
@@ -1004,7 +991,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             // a NaN that the sum does not have: from a hidden key's values?
             uint64_t seen = pack2(0.0f, 0.0f);
 #pragma unroll 1
-            for (uint32_t i = 0; i < D / 32; ++i) {
+            for (uint32_t i = 0; i < D / 64; ++i) {
                 uint32_t o[32];
                 tmem_ld32(o_at + i * 32, o);
                 tmem_wait_ld();
@@ -1023,11 +1010,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 const float ref1 = __shfl_sync(0xFFFFFFFFu, ref, src), inv1 = __shfl_sync(0xFFFFFFFFu, inv, src);
                 uint16_t *const out1 = whole ? (uint16_t *)p.a.d_out + (uint64_t)t * p.a.out_stride[0] + (uint64_t)h * p.a.out_stride[1] : nullptr;
                 visible_row<T, D>(&p, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)t * p.a.q_stride[0] + (uint64_t)h * p.a.q_stride[1], from, to,
-                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0));
+                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half);
             }
             if (whole) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = 0; i < D / 64; ++i) {
                     uint32_t o[32];
                     tmem_ld32(o_at + i * 32, o);
                     tmem_wait_ld();
@@ -1036,27 +1023,43 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         float x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = any ? __uint_as_float(o[8 * j + e]) * inv : 0.0f;
-                        if (mine) *(uint4 *)(out + i * 32 + j * 8) = narrow8<T>(x);
+                        if (mine) *(uint4 *)(out + half * (D / 2) + i * 32 + j * 8) = narrow8<T>(x);
                     }
                 }
-                if (row < rows && p.a.d_lse_or_null)
+                if (half == 0 && row < rows && p.a.d_lse_or_null)
                     p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any ? (l > 0.0f || l != l ? (ref + log2f(l)) * kLn2 : -INFINITY) : -INFINITY;
             } else {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = 0; i < D / 64; ++i) {
                     uint32_t o[32];
                     tmem_ld32(o_at + i * 32, o);
                     tmem_wait_ld();
                     if (mine)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *(uint4 *)(part + S::part_o(m_tile, i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            *(uint4 *)(part + S::part_o(m_tile, half * (D / 8) + i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
-                if (row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
+                if (half == 0 && row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
             }
         }
         tc_fence_before();
     }
+    if (wid == S::kStatusWarp) {  // the requests' statuses, a request per CTA at a time
+        for (uint32_t r = blockIdx.x; r < p.kv.n_reqs; r += gridDim.x) {
+            const Request q = load_request(p.kv, r);
+            sz_status st = q.status;
+            if (st == SZ_OK && q.n > 0 && q.kv > 0) {
+                int32_t begin, stop;
+                key_range(p, q, 0, q.n, &begin, &stop);
+                st = check_pages(p.kv, r, (uint32_t)begin / p.kv.page_tokens, (uint32_t)(q.kv - 1) / p.kv.page_tokens + 1);
+            }
+            if (lane == 0) {
+                p.status[r] = st;
+                __threadfence();  // a CTA that fails sets timed_out, then the statuses
+                if (*(volatile unsigned long long *)p.timed_out == p.call) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
+            }
+    }
+        }
     // ------------------------------------------------------------------ end
     __syncthreads();
     if (failed) {  // rows may be unfinished: no result of this call stands
