@@ -151,13 +151,6 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
-#ifndef SZ_BU
-#define SZ_BU (kM == 1 ? 1 : 2)
-#endif
-#ifndef SZ_POLY
-#define SZ_POLY 4
-#endif
-constexpr int kPolyEvery = SZ_POLY;  // every so many pairs of weights take the polynomial
 constexpr uint32_t kWholeTiles = 6;                     // blocks up to this long are not split when there is a CTA for each
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
@@ -172,19 +165,32 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kHalves * kHalfBytes;
     static constexpr int kQueries = D == 64 ? 2 : 1;  // blocks whose queries are in shared memory at a time
     static constexpr int kSlots = kM == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6);
-    // Warps.  A softmax warp holds 32 rows and half of a key tile's columns;
-    // which lanes of tensor memory it reaches goes by its number modulo 4.
-    //   kM = 2: 0..15 softmax (row tile, half, 32 rows), 16, 17 products, 18 copies of Q and K, 19 of V
-    //   kM = 1: 0, 1 and 4, 5 softmax, 2 products, 3 and 6 copies, 7 statuses
-    static constexpr uint32_t kQuads = kRows / 32;  // warps per half of a row tile
-    static constexpr uint32_t kMmaWarp = kM == 2 ? 16 : 2, kKeyWarp = kM == 2 ? 18 : 3, kValueWarp = kM == 2 ? 19 : 6;
-    static constexpr uint32_t kStatusWarp = kM == 2 ? kValueWarp : 7;
-    static constexpr int kThreads = kM == 2 ? 640 : 256;
+    // Warps.  Which lanes of tensor memory a warp reaches goes by its number
+    // modulo 4.  A softmax warp holds 32 rows: with two row tiles all 128
+    // columns of a key tile (the row tiles take turns on the tensor cores, and
+    // more warps would only share the same arithmetic units), with one row
+    // tile half of them, which shortens the chain from tile to tile.
+    //   kM = 2: 0..7 softmax, 8 (and 9) products, 9 (or 11) statuses, 10 copies of Q and K, 11 of V
+    //   kM = 1: 0, 1 and 4, 5 softmax (4, 5: columns 64 ..), 2 products, 3 and 6 copies, 7 statuses
+    static constexpr uint32_t kQuads = kRows / 32;  // warps that hold a row tile's rows
+    static constexpr bool kPaired = kM == 1;
+    static constexpr uint32_t kMmaWarp = kM == 2 ? 8 : 2, kKeyWarp = kM == 2 ? 10 : 3, kValueWarp = kM == 2 ? 11 : 6;
+    // One warp issues the products of both row tiles of 128 channels, which so
+    // fall into turns: the products of one run while the other's softmax works
+    // (4,096 x 32,768 chunk: 1.66 ms, with a warp each 1.86).  Products of 64
+    // channels take half as long as the softmax, and a warp each lets neither
+    // wait for the other's weights (ragged prompts: 78 us, with one warp 85).
+    static constexpr uint32_t kMmaWarps = kM == 2 && D == 64 ? 2 : 1;
+    static constexpr uint32_t kStatusWarp = kM == 1 ? 7 : kMmaWarps == 2 ? kValueWarp : 9;
+    static constexpr int kThreads = kM == 2 ? 384 : 256;
+    // Registers a thread of the softmax and of the other warps (kM = 2): three
+    // warpgroups launched with 168 each, 2 * 208 + 88 = 3 * 168.
+    static constexpr int kManyRegs = 208, kFewRegs = 88;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;
     static constexpr uint32_t kQueryHalf = kRows * kRowBytes, kQueryTile = kHalves * kQueryHalf, kQueryBytes = kM * kQueryTile;
     static constexpr uint32_t kData = kQueries * kQueryBytes + kSlots * kTileBytes;
-    static constexpr uint32_t kControlBytes = 384 + 2 * 4 * kM * kRows;  // barriers, the CTA's share, exchanged numbers
+    static constexpr uint32_t kControlBytes = kM == 2 ? 768 : 384 + 2 * 4 * kRows;  // barriers, the CTA's share, exchanged numbers
     static constexpr uint32_t kSmem = kData + kControlBytes;
     // A part of a block: per row tile 4 channels of all rows, the next 4, ...
     // (so that threads that hold a row each write and read side by side),
@@ -253,7 +259,7 @@ __device__ __forceinline__ uint32_t block_count(const TensorArgs &p, const Reque
 // What a block costs beside its tiles (queries, first scores, output), in
 // tiles: the units of a block begin with as many that hold no tile.
 template <int kM>
-constexpr uint32_t kBlockUnits = SZ_BU;
+constexpr uint32_t kBlockUnits = kM == 1 ? 1 : 3;
 
 // Where a CTA stands in the order of units.
 struct Cursor {
@@ -375,8 +381,8 @@ struct PlanShared {
 
 // What the search for it exchanges between warps.
 struct PlanScratch {
-    uint64_t units[20], blocks[20];
-    uint32_t most[20];
+    uint64_t units[12], blocks[12];
+    uint32_t most[12];
 };
 
 // This CTA's share of the units, found by all of its threads.
@@ -536,16 +542,23 @@ __device__ __forceinline__ bool pair_any(uint32_t id, bool x) {
     return any != 0;
 }
 
+// Whether any row of the warp, or of the pair, asks for another reference.
+template <bool kPaired>
+__device__ __forceinline__ bool asks(uint32_t pair, bool x) {
+    if constexpr (kPaired) return pair_any(pair, x);
+    return __any_sync(0xFFFFFFFFu, x) != 0;
+}
+
 // One row's accumulator over the visible ones of keys [from, to), by one
 // warp: sum 2^(c s_j - ref) v_j.  A key hidden from a row has weight 0 in the
 // products, and 0 * inf there is NaN: a row whose accumulator holds a NaN
 // while its sum does not is computed again here from the keys it sees alone.
 // (If one of those is the reason, the loop ends when every channel is NaN.)
-// Writes half of the channels of the scaled 16-bit row to `out`, or of the
-// 32-bit one to `part`.
+// Writes channels 8 * own_begin .. (8 * own of them) of the scaled 16-bit row
+// to `out`, or of the 32-bit one to `part`.
 template <typename T, int D>
 __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32_t kv_head, const uint16_t *q, int32_t from, int32_t to,
-                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t half) {
+                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t own_begin, uint32_t own) {
     constexpr uint32_t kLanes = D / 8, kGroups = 32 / kLanes;  // lanes per key, keys at a time
     const sz_paged_kv &kv = p->kv;
     const uint32_t lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
@@ -585,7 +598,7 @@ __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32
     for (uint32_t d = kLanes; d < 32; d <<= 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xFFFFFFFFu, o[i], d);
-    if (group != 0 || l / (kLanes / 2) != half) return;
+    if (group != 0 || l < own_begin || l >= own_begin + own) return;
     if (out) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] *= inv;
@@ -610,7 +623,7 @@ struct Control {  // behind the tiles in shared memory
     uint32_t tmem, failed;
     union {
         PlanScratch scratch;
-        float swap[2][kM * Shape<D, kM>::kRows];  // between the two halves of a row: maxima, sums
+        float swap[2][Shape<D, kM>::kPaired ? Shape<D, kM>::kRows : 1];  // between the two halves of a row: maxima, sums
     };
 };
 
@@ -636,17 +649,17 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint32_t smem0 = smem_u32(raw);
     const uint32_t ring0 = smem0 + S::kQueries * S::kQueryBytes;
     constexpr uint32_t kMmaWarp = S::kMmaWarp;
-    const bool softmax = kM == 2 ? wid < 16 : (wid & 3) < 2 && wid < 6;
+    const bool softmax = kM == 2 ? wid < 8 : (wid & 3) < 2 && wid < 6;
 
     if (wid == kMmaWarp) tmem_alloc(&control.tmem, S::kColumns);
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(&bars.full[i], 1);
-            mbar_init(&bars.empty[i], kM);
+            mbar_init(&bars.empty[i], S::kMmaWarps);
         }
         for (int i = 0; i < S::kQueries; ++i) {
             mbar_init(&bars.q_full[i], 1);
-            mbar_init(&bars.q_empty[i], kM);
+            mbar_init(&bars.q_empty[i], S::kMmaWarps);
         }
         for (int x = 0; x < kM; ++x) {
             mbar_init(&bars.s_full[x], 1);
@@ -690,6 +703,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
     if (!softmax) {
+        if constexpr (kM == 2) give_registers<S::kFewRegs>();
         if (wid == S::kKeyWarp || wid == S::kValueWarp) {
         // ------------------------------------- copies: Q and K, or V
         const bool one = elect_one();
@@ -773,94 +787,102 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             for (uint32_t u = pieces > S::kQueries ? pieces - S::kQueries : 0; u < pieces; ++u)
                 mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, limit);
         }
-        } else if (wid >= kMmaWarp && wid < kMmaWarp + kM) {
+        } else if (wid >= kMmaWarp && wid < kMmaWarp + S::kMmaWarps) {
         // ---------------------------------------------------------- products
-        // One warp per row tile: issuing waits for the tensor cores' queue, and
-        // what a warp does between its products then costs the other's nothing.
         const bool one = elect_one();
-        const uint32_t m = wid - kMmaWarp;
-        const uint32_t q_lo = desc_lo(smem0, 16) + m * (S::kQueryTile >> 4), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
-        const uint32_t s_at = tmem + m * 128, o_at = tmem + kM * 128 + m * D;
-        uint64_t *const s_full = &bars.s_full[m], *const p_full = bars.p_full[m], *const pv_done = &bars.pv_done[m];
-        uint32_t done = 0;  // key tiles of this row tile
+        const uint32_t q_lo = desc_lo(smem0, 16), k_lo = desc_lo(ring0, 16), v_lo = desc_lo(ring0, kHalfBytes);
+        uint32_t done = 0, done2 = 0;  // key tiles of this warp's row tile, or of the first and the second
         uint32_t slot = 0, phase = 0;  // of the ring, at the next K or V
-        auto pass = [&] {  // to the next of the ring
+        auto pass = [&] {              // to the next of the ring
             if (++slot == S::kSlots) slot = 0, phase ^= 1;
+        };
+        const uint32_t mine = wid - kMmaWarp;
+        auto each = [&](auto f) {  // row tile of this warp's
+            if constexpr (S::kMmaWarps == 2) {
+                f(mine);
+            } else {
+#pragma unroll
+                for (uint32_t m = 0; m < kM; ++m) f(m);
+            }
         };
         for (uint32_t piece = 0; same(*fail) == 0; ++piece) {
             if (same(next_piece<kM>(p, cur, w) ? 1u : 0u) == 0) break;
             const int32_t t_begin = (int32_t)same((uint32_t)w.t0), t_end = (int32_t)same((uint32_t)w.t1), kv = (int32_t)same((uint32_t)w.q.kv);
-            const bool active = m == 0 || same((uint32_t)w.q.n - w.block * kM * p.tile_tokens > p.tile_tokens ? 1u : 0u) != 0;
+            const uint32_t tiles = same(kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens ? 1u : 2u);  // row tiles in use
             const uint32_t buf = piece % S::kQueries;
-            const uint32_t qa = q_lo + buf * (S::kQueryBytes >> 4);
-            auto score = [&] {  // S = Q K^T, K at `slot`
-                const uint32_t b = k_lo + slot * (S::kTileBytes >> 4);
+            auto score = [&](uint32_t m) {  // S_m = Q_m K^T, K at `slot`
+                const uint32_t qa = q_lo + buf * (S::kQueryBytes >> 4) + m * (S::kQueryTile >> 4), b = k_lo + slot * (S::kTileBytes >> 4);
                 if (one) {
-                    if (active) {
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t half = (uint32_t)(i / 4), off = (uint32_t)(i % 4) * 32 >> 4;
-                            mma_smem(s_at, full_desc(qa + half * (S::kQueryHalf >> 4) + off), full_desc(b + half * (kHalfBytes >> 4) + off), kScoreWord, i > 0);
-                        }
-                        mma_commit(s_full);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t half = (uint32_t)(i / 4), off = (uint32_t)(i % 4) * 32 >> 4;
+                        mma_smem(tmem + m * 128, full_desc(qa + half * (S::kQueryHalf >> 4) + off), full_desc(b + half * (kHalfBytes >> 4) + off), kScoreWord, i > 0);
                     }
-                    mma_commit(&bars.empty[slot]);
+                    mma_commit(&bars.s_full[m]);
                 }
                 __syncwarp();
-                pass();
             };
             wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, fail, limit);
             wait_or_fail(&bars.full[slot], phase, fail, limit);
             tc_fence_after();
-            score();
+            each([&](uint32_t m) {
+                if (m < tiles) score(m);
+            });
+            if (one) mma_commit(&bars.empty[slot]);
+            pass();
             for (int32_t t = t_begin; t < t_end; ++t) {
                 const uint32_t v_slot = slot;
+                const bool more = t + 1 < t_end;
                 wait_or_fail(&bars.full[slot], phase, fail, limit);
                 pass();
-                if (t + 1 < t_end)  // the next K now, so that nothing is waited for between the products
+                if (more)  // the next K now, so that nothing is waited for between the products
                     wait_or_fail(&bars.full[slot], phase, fail, limit);
                 else if (one)
                     mma_commit(&bars.q_empty[buf]);
-                if (active) {
-                    // keys behind the last token in this tile's last page: their
-                    // weights are 0, so their values must be finite
-                    const int32_t z0 = kv - t * (int32_t)p.key_tile;
-                    if (z0 > 0 && z0 < (int32_t)p.key_tile) {
-                        const int32_t page = (int32_t)p.kv.page_tokens;
-                        const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
-                        const uint32_t vb = ring0 + v_slot * S::kTileBytes;
-                        for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
-                            const uint32_t chunk = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + chunk * 16), "r"(0)
-                                         : "memory");
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                // keys behind the last token in this tile's last page: their
+                // weights are 0, so their values must be finite
+                const int32_t z0 = kv - t * (int32_t)p.key_tile;
+                if (z0 > 0 && z0 < (int32_t)p.key_tile) {
+                    const int32_t page = (int32_t)p.kv.page_tokens;
+                    const int32_t z1 = (int32_t)min((int64_t)p.key_tile, ((int64_t)kv + page - 1) / page * page - (int64_t)t * p.key_tile);
+                    const uint32_t vb = ring0 + v_slot * S::kTileBytes;
+                    for (int32_t i = (int32_t)lane; i < (z1 - z0) * S::kHalves * 8; i += 32) {
+                        const uint32_t chunk = i % 8, half = i / 8 % S::kHalves, row = (uint32_t)(z0 + i / 8 / S::kHalves);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vb + half * kHalfBytes + row * kRowBytes + chunk * 16), "r"(0)
+                                     : "memory");
                     }
-                    const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
-#pragma unroll
-                    for (uint32_t part = 0; part < 2; ++part) {  // the weights of 64 keys each
-                        wait_or_fail(&p_full[part], done & 1, fail, limit);
-                        tc_fence_after();
-                        if (one) {
-#pragma unroll
-                            for (uint32_t i = 0; i < 4; ++i)
-                                mma_tmem(o_at, s_at + part * 64 + i * 8, full_desc(vb + (part * 4 + i) * (16 * kRowBytes >> 4)), kOutWord,
-                                         (t > t_begin || part + i > 0) ? 1u : 0u);
-                            if (part == 1) mma_commit(pv_done);
-                        }
-                        __syncwarp();
-                    }
-                    ++done;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
                 }
-                if (one) mma_commit(&bars.empty[v_slot]);
-                if (t + 1 < t_end) score();
+                const uint32_t vb = v_lo + v_slot * (S::kTileBytes >> 4);
+                each([&](uint32_t m) {
+                    if (m < tiles) {
+#pragma unroll
+                        for (uint32_t part = 0; part < 2; ++part) {  // the weights of 64 keys each
+                            wait_or_fail(&bars.p_full[m][part], (S::kMmaWarps == 1 && m == 1 ? done2 : done) & 1, fail, limit);
+                            tc_fence_after();
+                            if (one) {
+#pragma unroll
+                                for (uint32_t i = 0; i < 4; ++i)
+                                    mma_tmem(tmem + kM * 128 + m * D, tmem + m * 128 + part * 64 + i * 8, full_desc(vb + (part * 4 + i) * (16 * kRowBytes >> 4)),
+                                             kOutWord, (t > t_begin || part + i > 0) ? 1u : 0u);
+                                if (part == 1) mma_commit(&bars.pv_done[m]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (one && (S::kMmaWarps == 2 || m + 1 == kM)) mma_commit(&bars.empty[v_slot]);
+                    if (more && m < tiles) score(m);
+                });
+                if (S::kMmaWarps == 2) done += mine < tiles ? 1 : 0; else ++done, done2 += tiles > 1 ? 1 : 0;
+                if (more && one) mma_commit(&bars.empty[slot]);
+                if (more) pass();
             }
         }
         if (*fail) {  // products under way must end before their memory is given back
             if (one) {
-                mma_commit(&bars.drain[m]);
-                mbar_wait(&bars.drain[m], 0, limit);
+                mma_commit(&bars.drain[mine]);
+                mbar_wait(&bars.drain[mine], 0, limit);
             }
             __syncwarp();
         }
@@ -868,13 +890,16 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     } else {
         // ----------------------------------------------------------- softmax
 
-        const uint32_t m_tile = kM == 2 ? wid / 8 : 0, half = wid / 4 & 1, quad = wid & 3;
+        if constexpr (kM == 2) take_registers<S::kManyRegs>();
+        constexpr uint32_t kParts = S::kPaired ? 1 : 2;    // of 64 columns, per warp
+        constexpr uint32_t kOwn = S::kPaired ? D / 2 : D;  // channels that a warp rescales and writes
+        const uint32_t m_tile = kM == 2 ? wid / 4 : 0, half = S::kPaired ? wid / 4 : 0, quad = wid & 3;
         const uint32_t row = quad * 32 + lane;
         const uint32_t lanes = quad * 32;  // of tensor memory
-        const uint32_t pair = 1 + m_tile * 4 + quad;  // barrier of the two warps that share rows
+        const uint32_t pair = 1 + quad;    // barrier of the two warps that share rows
         const uint32_t s_at = tmem + (lanes << 16) + m_tile * 128 + half * 64;
-        const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D + half * (D / 2);  // this warp's half of the channels
-        float *const swap_mine = &control.swap[half][m_tile * S::kRows + row], *const swap_other = &control.swap[half ^ 1][m_tile * S::kRows + row];
+        const uint32_t o_at = tmem + (lanes << 16) + kM * 128 + m_tile * D + half * kOwn;
+        float *const swap_mine = &control.swap[half][S::kPaired ? row : 0], *const swap_other = &control.swap[half ^ 1][S::kPaired ? row : 0];
         const uint32_t my_token = row / p.group, my_head = row % p.group;
         uint32_t n = 0;  // tiles done by this row tile
         while (next_piece<kM>(p, cur, w)) {
@@ -891,29 +916,34 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 tc_fence_after();
                 if (warp_live) {
                     // this row's visible columns; all of them in most tiles
-                    const int32_t k0 = t * (int32_t)p.key_tile + (int32_t)half * 64;
-                    const int32_t from = begin - k0, to = min(stop - k0, (int32_t)p.key_tile - (int32_t)half * 64);
-                    const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < 64) != 0;
-                    float high;
-                    {
-                        uint32_t s[64];
-                        tmem_ld64(s_at, s);
-                        tmem_wait_ld();
-                        if (masked) hide(s, from, to);
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const int32_t k0 = t * (int32_t)p.key_tile;
+                    const int32_t from = begin - k0 - (int32_t)half * 64, to = min(stop - k0, (int32_t)p.key_tile) - (int32_t)half * 64;
+                    const bool masked = __any_sync(0xFFFFFFFFu, from > 0 || to < (int32_t)kParts * 64) != 0;
+                    uint32_t s[kParts][64];
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tmem_ld64(s_at, s[0]);
+                    tmem_wait_ld();
+                    if constexpr (kParts == 2) tmem_ld64(s_at + 64, s[1]);
+#pragma unroll
+                    for (uint32_t part = 0; part < kParts; ++part) {
+                        if (part) tmem_wait_ld();
+                        if (masked) hide(s[part], from - (int32_t)part * 64, to - (int32_t)part * 64);
 #pragma unroll
                         for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], __uint_as_float(s[j + 2 * i]), __uint_as_float(s[j + 2 * i + 1]));
-                        high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+                            for (int i = 0; i < 4; ++i)
+                                top[i] = max3(top[i], __uint_as_float(s[part][j + 2 * i]), __uint_as_float(s[part][j + 2 * i + 1]));
                     }
-                    // Both halves of a row use one reference: it moves when
-                    // either asks, which is at first and then rarely.
+                    float high = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+                    // A row has one reference: it moves at first and then
+                    // rarely, for both of a pair of warps when either asks.
                     const bool begins = t == w.t0;
-                    if (begins || pair_any(pair, (high - m) * p.c > kRescaleAt)) {
-                        *swap_mine = high;
-                        pair_sync(pair);
-                        high = fmaxf(high, *swap_other);
+                    if (begins || asks<S::kPaired>(pair, (high - m) * p.c > kRescaleAt)) {
+                        if constexpr (S::kPaired) {
+                            *swap_mine = high;
+                            pair_sync(pair);
+                            high = fmaxf(high, *swap_other);
+                        }
                         if (begins) {
                             m = high;
                         } else {
@@ -925,7 +955,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             if (rise) m = high;
                             sum = mul2(sum, pack2(f, f));
 #pragma unroll 1
-                            for (uint32_t i = 0; i < D / 32; ++i) {
+                            for (uint32_t i = 0; i < kOwn / 16; ++i) {
                                 uint32_t o[16];
                                 tmem_ld16(o_at + i * 16, o);
                                 tmem_wait_ld();
@@ -935,52 +965,51 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             }
                             tmem_wait_st();
                             tc_fence_before();
-                            pair_sync(pair);  // the other half's channels too, before any weight is handed over
+                            if constexpr (S::kPaired) pair_sync(pair);  // the other's channels too, before any weight is handed over
                         }
                     }
                     const float ref = m == -INFINITY ? 0.0f : m * p.c;
                     const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
                     uint64_t sum1 = pack2(0.0f, 0.0f);
-                    // The scores are read again: tensor memory is close by, and
-                    // fewer registers let more warps work.  Weights of columns
-                    // 32 i .. take columns 16 i .. of the half.
-#pragma unroll 1
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        uint32_t s[32], w16[16];
-                        tmem_ld32(s_at + i * 32, s);
-                        tmem_wait_ld();
-                        if (masked) hide(s, from - (int32_t)i * 32, to - (int32_t)i * 32);
+#pragma unroll
+                    for (uint32_t i = 0; i < kParts * 2; ++i) {  // weights of 64 columns take the first 32 of them
+                        uint32_t w16[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const uint64_t x = fma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, ref2);
-                            uint64_t e;
-                            if (j % kPolyEvery == kPolyEvery - 1) {
-                                e = exp2_poly2(x);
-                            } else {
-                                const float2 f = unpack2(x);
-                                e = pack2(exp2_fast(f.x), exp2_fast(f.y));
-                            }
-                            if (j & 1) sum1 = add2(sum1, e); else sum = add2(sum, e);
-                            const float2 f = unpack2(e);
-                            w16[j] = Half2<T>::narrow(f.x, f.y);
+                            const int at = (int)(i & 1) * 32 + 2 * j;
+                            const uint64_t x = fma2(pack2(__uint_as_float(s[i / 2][at]), __uint_as_float(s[i / 2][at + 1])), c2, ref2);
+                            const float2 y = unpack2(x), e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                            if (j & 1) sum1 = add2(sum1, pack2(e.x, e.y)); else sum = add2(sum, pack2(e.x, e.y));
+                            w16[j] = Half2<T>::narrow(e.x, e.y);
                         }
-                        tmem_st16(s_at + i * 16, w16);
+                        tmem_st16(s_at + (i / 2) * 64 + (i & 1) * 16, w16);
+                        if (kParts == 2 && i == 1) {  // the first 64 keys' weights can go
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
+                        }
                     }
                     sum = add2(sum, sum1);
                     tmem_wait_st();
+                } else if (kParts == 2 && lane == 0) {
+                    mbar_arrive(&bars.p_full[m_tile][0]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[m_tile][half]);
+                if (lane == 0) mbar_arrive(&bars.p_full[m_tile][kParts == 2 ? 1 : half]);
             }
             wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
             tc_fence_after();
             if (!warp_live) continue;
             const float2 both = unpack2(sum);
-            *swap_mine = both.x + both.y;
-            pair_sync(pair);
-            const float l = half ? *swap_other + *swap_mine : *swap_mine + *swap_other;
-            pair_sync(pair);  // read by both before it is written again
+            float l = both.x + both.y;
+            if constexpr (S::kPaired) {
+                *swap_mine = l;
+                pair_sync(pair);
+                l = half ? *swap_other + l : l + *swap_other;
+                pair_sync(pair);  // read by both before it is written again
+            }
             bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
             const float ref = m * p.c;  // log2 units
@@ -991,7 +1020,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             // a NaN that the sum does not have: from a hidden key's values?
             uint64_t seen = pack2(0.0f, 0.0f);
 #pragma unroll 1
-            for (uint32_t i = 0; i < D / 64; ++i) {
+            for (uint32_t i = 0; i < kOwn / 32; ++i) {
                 uint32_t o[32];
                 tmem_ld32(o_at + i * 32, o);
                 tmem_wait_ld();
@@ -1010,11 +1039,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 const float ref1 = __shfl_sync(0xFFFFFFFFu, ref, src), inv1 = __shfl_sync(0xFFFFFFFFu, inv, src);
                 uint16_t *const out1 = whole ? (uint16_t *)p.a.d_out + (uint64_t)t * p.a.out_stride[0] + (uint64_t)h * p.a.out_stride[1] : nullptr;
                 visible_row<T, D>(&p, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)t * p.a.q_stride[0] + (uint64_t)h * p.a.q_stride[1], from, to,
-                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half);
+                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half * (kOwn / 8), kOwn / 8);
             }
             if (whole) {
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
+                for (int i = 0; i < (int)kOwn / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld32(o_at + i * 32, o);
                     tmem_wait_ld();
@@ -1023,21 +1052,21 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                         float x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = any ? __uint_as_float(o[8 * j + e]) * inv : 0.0f;
-                        if (mine) *(uint4 *)(out + half * (D / 2) + i * 32 + j * 8) = narrow8<T>(x);
+                        if (mine) *(uint4 *)(out + half * kOwn + i * 32 + j * 8) = narrow8<T>(x);
                     }
                 }
                 if (half == 0 && row < rows && p.a.d_lse_or_null)
                     p.a.d_lse_or_null[(uint64_t)token * p.a.q_heads + head] = any ? (l > 0.0f || l != l ? (ref + log2f(l)) * kLn2 : -INFINITY) : -INFINITY;
             } else {
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
+                for (int i = 0; i < (int)kOwn / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld32(o_at + i * 32, o);
                     tmem_wait_ld();
                     if (mine)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *(uint4 *)(part + S::part_o(m_tile, half * (D / 8) + i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            *(uint4 *)(part + S::part_o(m_tile, half * (kOwn / 4) + i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
                 if (half == 0 && row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
             }

@@ -78,18 +78,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
                  "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[N]) {
-    static_assert(N >= 32, "32 values");
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
 // ----------------------------------------------------- matrix instructions
 // Shared-memory operands: rows (or columns) of 64 16-bit values, 128 bytes,
 // eight to a 1,024-byte group, 16-byte pieces swizzled inside it as the
@@ -125,6 +113,17 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 
 // -------------------------------------------------------------- arithmetic
+// Warpgroups of 4 warps trade registers; the shares add up to what the block
+// was launched with.
+template <int kCount>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+template <int kCount>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCount));
+}
+
 // Two 32-bit numbers in one instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -156,41 +155,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// 2^x of two numbers at most 128, without the special-function unit (16
-// results a clock and SM, which a softmax of tensor-core scores outruns).
-// x = i + f with i the nearest integer (Cody and Waite's reduction, by adding
-// and taking away 1.5 * 2^23); 2^f on [-1/2, 1/2] by the degree-5 polynomial
-// with constant term 1 whose largest relative error is least (linear
-// programme over 4,001 Chebyshev points: 8e-8; 1.6e-7 as evaluated in 32
-// bits); 2^i by its exponent field.  x is held at or above -127, where f = 0
-// and the exponent field 0 give exactly 0; a NaN stays a NaN.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-    const float2 x = unpack2(x2);
-    x2 = pack2(max_nan(x.x, -127.0f), max_nan(x.y, -127.0f));
-    const uint64_t magic = pack2(12582912.0f, 12582912.0f), back = pack2(-12582912.0f, -12582912.0f);
-    const uint64_t t = add2(x2, magic);
-    const uint64_t f = fma2(add2(t, back), pack2(-1.0f, -1.0f), x2);
-    uint64_t p = pack2(0.0013274633092805743f, 0.0013274633092805743f);
-    p = fma2(p, f, pack2(0.009671961888670921f, 0.009671961888670921f));
-    p = fma2(p, f, pack2(0.055506784468889236f, 0.055506784468889236f));
-    p = fma2(p, f, pack2(0.24022234976291656f, 0.24022234976291656f));
-    p = fma2(p, f, pack2(0.6931470632553101f, 0.6931470632553101f));
-    p = fma2(p, f, pack2(1.0f, 1.0f));
-    const float2 ti = unpack2(t);
-    const float s0 = __uint_as_float((__float_as_uint(ti.x) << 23) + 0x3F800000u);
-    const float s1 = __uint_as_float((__float_as_uint(ti.y) << 23) + 0x3F800000u);
-    return mul2(p, pack2(s0, s1));
 }
 
 }  // namespace sz
