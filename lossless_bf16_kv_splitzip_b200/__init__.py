@@ -508,4 +508,5 @@ class BatchPlan:
         return self.container[off: off + size].cpu().numpy()
 
 
+from . import paged  # noqa: E402
 from .paged import append_kv, paged_attention, rope_frequencies  # noqa: E402

@@ -1,4 +1,5 @@
-"""Build libsplitzip.so in-tree with nvcc for sm_100a (B200)."""
+"""Build libsplitzip.so in-tree with nvcc for sm_100a (B200), and the compiled
+part of the Python binding (_binding.so) with g++ against torch's headers."""
 from __future__ import annotations
 
 import glob
@@ -10,6 +11,8 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 LIB_PATH = os.path.join(PKG, "libsplitzip.so")
+BINDING_PATH = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "sz_binding.cpp")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -52,3 +55,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.check_call(cmd)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
+
+
+def binding_is_stale() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return True
+    t = os.path.getmtime(BINDING_PATH)
+    return any(os.path.getmtime(p) > t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "splitzip.h")))
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/sz_binding.cpp into _binding.so (skipped when up to date)."""
+    if not force and not binding_is_stale():
+        return BINDING_PATH
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    dirs = include_paths() + [sysconfig.get_paths()["include"], INCLUDE, os.path.join(cuda, "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += ["-isystem" + d for d in dirs] + [BINDING_SOURCE, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
