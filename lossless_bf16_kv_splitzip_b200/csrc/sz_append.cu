@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(32 * (kCount ? kCountWarps : kAppendWarps), kC
         uint32_t t = t_begin;
         while (t < t_end) {  // the same run of tokens in every warp
             const uint32_t r = warp_request_of(kv, t, lane);
-            uint32_t stop = t_end, k_row = 0, v_row = 0;
+            uint32_t stop = t + 1, k_row = 0, v_row = 0;  // alone, if it is a row of no request
             bool counted = false;
             Request q{};
             if (r < kv.n_reqs) {
@@ -307,8 +307,6 @@ __global__ void __launch_bounds__(32 * (kCount ? kCountWarps : kAppendWarps), kC
                 if (owns(q, t)) {
                     stop = umin32(t_end, (uint32_t)(q.q0 + q.n));
                     counted = hist_rows(p, r, k_row, v_row);
-                } else {
-                    stop = t + 1;  // a row of no request
                 }
             }
             if (counted) {
@@ -352,7 +350,7 @@ static cudaError_t launch_append_lanes(AppendArgs &p, int sms, cudaStream_t s) {
     // A warp takes a token's heads in slices: as many warps as keep the SMs
     // busy (24 each), and no more, since each looks its token up anew.
     const uint64_t groups = div_up(heads, at_once);
-    const uint64_t per_warp = umax64(1, tokens * groups / ((uint64_t)sms * 24));
+    const uint64_t per_warp = umax64(div_up(groups, 65535), tokens * groups / ((uint64_t)sms * 24));
     p.slice_heads = (uint32_t)umin64(groups, per_warp) * at_once;
     p.tokens_per_block = kAppendWarps;
     const dim3 grid((uint32_t)umax64(1, div_up(tokens, kAppendWarps)), (uint32_t)div_up(heads, p.slice_heads));

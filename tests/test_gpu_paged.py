@@ -220,6 +220,23 @@ def test_waits_that_run_out_are_reported():
         assert not status.any() and torch.equal(again, good)
 
 
+@pytest.mark.parametrize("new,kv,dim", [([5] * 12, [40] * 12, 128), ([7], [200], 64), ([200], [200], 128), ([4, 3], [5000, 70], 128)], ids=str)
+def test_hidden_values_with_the_output_over_the_queries(new, kv, dim):
+    # such rows are computed from their queries once more, which stay until
+    # every warp that needs them has read them
+    b = Batch(new, kv, 8, 2, dim, 16, BF16)
+    k, v, table, q_begin, kv_len = b.cache()
+    for r, n in enumerate(kv):
+        v[int(b.table[r, (n - 1) // 16]), :, (n - 1) % 16] = math.inf
+    q = b.q.to(DEV)
+    apart, _, _ = sz.paged_attention(q, k, v, table, q_begin, kv_len)
+    assert int(torch.isfinite(apart).all(-1).all(-1).sum()) == b.rows - len(kv)
+    for _ in range(20):
+        over = q.clone()
+        sz.paged_attention(over, k, v, table, q_begin, kv_len, out=over)
+        assert torch.equal(over.view(torch.int16), apart.view(torch.int16))
+
+
 @pytest.mark.parametrize("layout", ["token_major", "one_pool", "rows_of_a_projection", "in_place"])
 @pytest.mark.parametrize("dim", [128, 40])
 def test_attention_layouts(layout, dim):
@@ -460,6 +477,66 @@ def test_append_into_chosen_histogram_rows():
     _, status = sz.append_kv(new, new, k, v, table, q_begin, kv_len, hists=hists, hist_rows=rows)
     assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID]
     assert int(hists.sum()) == 2 * 30 * 2 * 128 and int(hists[0].sum()) == int(hists.sum())
+
+
+@pytest.mark.parametrize("shape", APPENDS, ids=lambda s: "-".join(map(str, s[:6])).replace(" ", ""))
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_counting_changes_nothing_else(shape, interleaved):
+    new, kv, hq, hk, dim, page, dtype = shape
+    b = Batch(new, kv, hq, hk, dim, page, dtype, extra_rows=2)
+    rows = [torch.randn((b.rows, h, dim), generator=b.g).to(dtype).to(DEV) for h in (hq, hk, hk)]
+    w = (1 + 0.3 * torch.randn(dim, generator=b.g)).to(dtype).to(DEV)
+    freqs = sz.rope_frequencies(dim // 16 * 16, device=DEV)
+    got = []
+    for counted in (False, True):
+        k, v, table, q_begin, kv_len = b.cache()
+        hists = torch.zeros((2 * len(kv), 256), dtype=torch.int32, device=DEV) if counted else None
+        q_out = torch.full_like(rows[0], 3.0)
+        _, status = sz.append_kv(rows[1], rows[2], k, v, table, q_begin, kv_len, q=rows[0], q_out=q_out, rope_freqs=freqs,
+                                 rope_interleaved=interleaved, q_norm=w, k_norm=w, hists=hists)
+        assert not status.any()
+        got.append([x.view(torch.int16) for x in (k, v, q_out)])
+    for a, c in zip(*got):
+        assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("counted", [False, True])
+@pytest.mark.parametrize("ahead", [3, 400])
+def test_rows_that_no_request_has(counted, ahead):
+    # rows before the first request, and padding rows as requests that nothing
+    # is cached for: neither is written, and every other row is
+    n, dim = [5, 6, 40, 2], 64
+    k = torch.zeros((30, 2, 16, dim), dtype=BF16, device=DEV)
+    v = torch.zeros_like(k)
+    table = torch.randperm(30)[:20].view(4, 5).to(torch.int32).to(DEV)
+    q_begin = torch.tensor([ahead] + [ahead + sum(n[: i + 1]) for i in range(4)], dtype=torch.int32, device=DEV)
+    kv_len = torch.tensor([20, 0, 40, 9], dtype=torch.int32, device=DEV)
+    tokens = ahead + sum(n) + 7
+    new = torch.randn((tokens, 2, dim), device=DEV).to(BF16)
+    hists = torch.zeros((8, 256), dtype=torch.int32, device=DEV) if counted else None
+    q_out = torch.full((tokens, 4, dim), 3.0, dtype=BF16, device=DEV)
+    q = torch.randn((tokens, 4, dim), device=DEV).to(BF16)
+    _, status = sz.append_kv(new, new, k, v, table, q_begin, kv_len, q=q, q_out=q_out, hists=hists)
+    assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID, 0, 0]
+    mine = torch.zeros(tokens, dtype=torch.bool, device=DEV)
+    for r in (0, 2, 3):
+        for i in range(n[r]):
+            t, at = int(q_begin[r]) + i, int(kv_len[r]) - n[r] + i
+            mine[t] = True
+            assert torch.equal(k[int(table[r, at // 16]), :, at % 16], new[t]) and torch.equal(v[int(table[r, at // 16]), :, at % 16], new[t])
+    assert torch.equal(q_out[mine], q[mine]) and bool((q_out[~mine] == 3.0).all())
+    assert int((k != 0).any(-1).any(1).sum()) == int(mine.sum())
+    if counted:
+        assert hists.sum(1).cpu().tolist() == [2 * dim * m for m in (5, 0, 40, 2)] * 2
+    out = torch.full_like(q, 3.0)
+    _, _, status = sz.paged_attention(q, k, v, table, q_begin, kv_len, out=out)
+    assert status.cpu().tolist() == [0, 0, 0, 0]
+    pad = torch.arange(int(q_begin[1]), int(q_begin[2]))
+    assert not out[pad].any() and bool((out[:ahead] == 3.0).all()) and bool((out[int(q_begin[4]):] == 3.0).all())
+    lone, _, _ = sz.paged_attention(q[int(q_begin[2]): int(q_begin[3])], k, v, table[2:3], torch.tensor([0, 40], dtype=torch.int32, device=DEV),
+                                    kv_len[2:3])
+    got = out[int(q_begin[2]): int(q_begin[3])]
+    assert float((got.double() - lone.double()).abs().max()) <= 2.0 ** -6 * float(v.abs().max())  # each within 2^-7 of the largest value
 
 
 @pytest.mark.parametrize("layout", ["token_major", "rows_of_a_projection"])
