@@ -7,8 +7,9 @@
 // Exponentials are taken base 2 of scores scaled by log2(e).
 #include <atomic>
 #include <chrono>
-#include <random>
 #include <type_traits>
+
+#include <unistd.h>
 
 #include "sz_paged.cuh"
 #include "sz_tensor.cuh"
@@ -555,10 +556,13 @@ __device__ __forceinline__ bool asks(uint32_t pair, bool x) {
 // while its sum does not is computed again here from the keys it sees alone.
 // (If one of those is the reason, the loop ends when every channel is NaN.)
 // Writes channels 8 * own_begin .. (8 * own of them) of the scaled 16-bit row
-// to `out`, or of the 32-bit one to `part`.
+// to `out`, or of the 32-bit one to `part`; where `out` lies over the queries
+// and two warps share the row, `pair` is their barrier, and neither writes
+// before both have read.
 template <typename T, int D>
 __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32_t kv_head, const uint16_t *q, int32_t from, int32_t to,
-                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t own_begin, uint32_t own) {
+                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t own_begin, uint32_t own,
+                                         uint32_t pair) {
     constexpr uint32_t kLanes = D / 8, kGroups = 32 / kLanes;  // lanes per key, keys at a time
     const sz_paged_kv &kv = p->kv;
     const uint32_t lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
@@ -598,6 +602,7 @@ __device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32
     for (uint32_t d = kLanes; d < 32; d <<= 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xFFFFFFFFu, o[i], d);
+    if (pair) pair_sync(pair);
     if (group != 0 || l < own_begin || l >= own_begin + own) return;
     if (out) {
 #pragma unroll
@@ -1029,6 +1034,14 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             }
             const float2 seen2 = unpack2(seen);
             uint32_t odd = __ballot_sync(0xFFFFFFFFu, mine && seen2.x + seen2.y != seen2.x + seen2.y && l > 0.0f && *fail == 0);
+            const bool shared_rows = S::kPaired && whole && (const void *)p.a.d_out == p.a.d_q;
+            if constexpr (S::kPaired)
+                if (shared_rows && pair_any(pair, odd != 0)) {  // then both take the same rows
+                    *swap_mine = __uint_as_float(odd);
+                    pair_sync(pair);
+                    odd |= __float_as_uint(*swap_other);
+                    pair_sync(pair);
+                }
             if (odd >> lane & 1u) mine = false;
             while (odd) {
                 const int src = __ffs(odd) - 1;
@@ -1039,7 +1052,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 const float ref1 = __shfl_sync(0xFFFFFFFFu, ref, src), inv1 = __shfl_sync(0xFFFFFFFFu, inv, src);
                 uint16_t *const out1 = whole ? (uint16_t *)p.a.d_out + (uint64_t)t * p.a.out_stride[0] + (uint64_t)h * p.a.out_stride[1] : nullptr;
                 visible_row<T, D>(&p, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)t * p.a.q_stride[0] + (uint64_t)h * p.a.q_stride[1], from, to,
-                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half * (kOwn / 8), kOwn / 8);
+                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half * (kOwn / 8), kOwn / 8,
+                                  shared_rows ? pair : 0u);
             }
             if (whole) {
 #pragma unroll
@@ -1252,12 +1266,16 @@ static uint64_t tensor_workspace() {
     return 8 + ctas * sizeof(SplitRec) + 2 * 4ull * Shape<D, kM>::kPartFloats * ctas;
 }
 
-// A tag for a call's words in the workspace: 48 bits, from a random start, so
+// A tag for a call's words in the workspace: 48 bits, from a start of the
+// clocks and the process (nothing that can throw), so
 // that words of earlier calls, or of other memory, do not carry it.
 static unsigned long long next_call() {
     static std::atomic<unsigned long long> next{[] {
-        std::random_device r;
-        return ((unsigned long long)r() << 32 | r()) ^ (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count();
+        unsigned long long x = (unsigned long long)std::chrono::system_clock::now().time_since_epoch().count() ^
+                               (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() << 20 ^
+                               (unsigned long long)getpid() << 44;
+        x = (x ^ x >> 31) * 0x9E3779B97F4A7C15ull;  // every bit of the clocks reaches the 48 kept
+        return x ^ x >> 29;
     }()};
     for (;;)
         if (const unsigned long long tag = next.fetch_add(1) & 0xFFFFFFFFFFFFull) return tag;

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -62,6 +63,10 @@ void ints(const at::Tensor &t, const char *name, int64_t dims) {
         fail(PyExc_ValueError, "%s must be an int32 tensor of %d dimension(s) with entries side by side", name, (int)dims);
 }
 
+void no_gradient(const at::Tensor &t, const char *name) {
+    if (t.requires_grad() && c10::GradMode::is_enabled()) fail(PyExc_ValueError, "%s requires a gradient, and this operator has none", name);
+}
+
 // Rows [tokens, heads, dim]; returns the heads.
 uint32_t rows(const at::Tensor &t, const char *name, at::ScalarType type, int64_t tokens, int64_t dim, uint64_t (&stride)[2]) {
     if (t.scalar_type() != type || t.dim() != 3 || t.size(0) != tokens || t.size(2) != dim)
@@ -69,7 +74,7 @@ uint32_t rows(const at::Tensor &t, const char *name, at::ScalarType type, int64_
              type_of(t), shape_of(t).c_str());
     if (t.size(1) > UINT32_MAX) fail(PyExc_ValueError, "%s has 2^32 heads or more", name);
     if (t.stride(2) != 1) fail(PyExc_ValueError, "%s needs its channels side by side", name);
-    if (t.requires_grad()) fail(PyExc_ValueError, "%s requires a gradient, and this operator has none", name);
+    no_gradient(t, name);
     stride[0] = (uint64_t)t.stride(0);
     stride[1] = (uint64_t)t.stride(1);
     return (uint32_t)t.size(1);
@@ -82,6 +87,8 @@ sz_paged_kv cache(const at::Tensor &k, const at::Tensor &v, const at::Tensor &ta
     if (k.dim() != 4 || v.sizes() != k.sizes())
         fail(PyExc_ValueError, "pages are two tensors [pages, heads, page tokens, channels] of one shape");
     if (k.stride(3) != 1 || v.stride(3) != 1) fail(PyExc_ValueError, "pages need their channels side by side");
+    no_gradient(k, "k_pages");
+    no_gradient(v, "v_pages");
     ints(table, "page_table", 2);
     ints(q_begin, "q_begin", 1);
     ints(kv_len, "kv_len", 1);
@@ -197,9 +204,13 @@ PyObject *append_kv(PyObject *const *a, Py_ssize_t n) {
     }
     if (positions && (positions->scalar_type() != at::kLong || positions->dim() != 1 || positions->size(0) != tokens || !positions->is_contiguous()))
         fail(PyExc_ValueError, "positions must be a contiguous int64 tensor [%lld]", (long long)tokens);
-    for (const at::Tensor *w : {q_norm, k_norm})
-        if (w && (w->scalar_type() != type || w->dim() != 1 || w->size(0) != dim || !w->is_contiguous()))
-            fail(PyExc_ValueError, "%s must be a contiguous %s tensor [%lld]", w == q_norm ? "q_norm" : "k_norm", toString(type), (long long)dim);
+    for (const at::Tensor *w : {q_norm, k_norm}) {
+        if (!w) continue;
+        const char *const name = w == q_norm ? "q_norm" : "k_norm";
+        if (w->scalar_type() != type || w->dim() != 1 || w->size(0) != dim || !w->is_contiguous())
+            fail(PyExc_ValueError, "%s must be a contiguous %s tensor [%lld]", name, toString(type), (long long)dim);
+        no_gradient(*w, name);
+    }
     if (hists) {
         if ((hists->scalar_type() != at::kInt && hists->scalar_type() != at::kUInt32) || hists->dim() < 1 || hists->size(-1) != 256 ||
             !hists->is_contiguous() || hists->numel() / 256 > UINT32_MAX)

@@ -198,3 +198,14 @@ def test_frequencies_in_bands():
     for bad in (0, 7):
         with pytest.raises(ValueError, match="rot_dim"):
             sz.rope_frequencies(bad)
+
+
+def test_gradients_are_refused_only_where_they_are_recorded():
+    t = tensors()
+    w = torch.nn.Parameter(torch.ones(t["q"].shape[2], dtype=t["q"].dtype))
+    with pytest.raises(ValueError, match="k_norm requires a gradient"):
+        put(t, k_norm=w)
+    with pytest.raises(ValueError, match="k_pages requires a gradient"):
+        attend({**t, "k_pages": t["k_pages"].clone().requires_grad_()})
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # the next check
+        put({**t, "k": t["k"].clone().requires_grad_()}, k_norm=w)
