@@ -23,7 +23,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 // ------------------------------------------------------------ any shape
 // One block per (new token, query head), any page size and head size: groups
 // of kLanes lanes (8 channels each) take keys in turn, each with its own
-// running softmax, joined at the end.
+// running softmax, joined at the end.  What bounds it is the latency of its
+// loads and the exchanges between lanes, and every row reads its keys anew:
+// it is there for the shapes that the tensor-core kernel does not take.
+// (Both on the same calls: one token over 333 keys 28 us, there 12; 5 tokens
+// of 8 requests over thousands of keys 1,680 and 45 us; ragged prompts 3,370
+// and 63 us.)
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(kGeneralThreads) attention_any_kernel(sz_paged_kv kv, sz_attention_args a, int32_t *status) {
     constexpr int kGroups = kGeneralThreads / kLanes;
@@ -137,12 +142,22 @@ static cudaError_t launch_any_t(const sz_paged_kv &kv, const sz_attention_args &
 // so a block's keys may be split over several of them (their parts are
 // joined afterwards, in order) and a CTA may serve several blocks.
 //
-// Warps: kM * 4 hold one row per thread (softmax); one issues the products;
-// one issues the copies.  Per row tile X and key tile: S_X = Q_X K^T into
-// tensor memory, the softmax threads replace S_X by P_X = exp2(c S - c m) in
-// 16 bits in the same columns, O_X += P_X V.  While one row tile's softmax
-// runs, the tensor cores work on the other's products (kM = 2) or on the
-// other CTA's of the SM (kM = 1).
+// Some warps hold rows, one per thread (softmax); others issue the products,
+// the copies of Q and K, and those of V (Shape gives their numbers).  Per row
+// tile X and key tile: S_X = Q_X K^T into tensor memory, the softmax threads
+// replace S_X by P_X = exp2(c S - c m) in 16 bits in the same columns, O_X +=
+// P_X V.  While one row tile's softmax runs, the tensor cores work on the
+// other's products (kM = 2) or on the other CTA's of the SM (kM = 1).
+//
+// What bounds it: with few rows per request the reading of the keys and
+// values (64 requests of one token, 735 MB: 129 us, 5.7 TB/s, 87 % of a copy;
+// one token over 131,071 keys: 93 us, 5.8 TB/s); with many the products and,
+// beside them, the softmax's exponentials and conversions (4,096 tokens over
+// 32,768 keys, 32 heads of 128: 1.66 ms, 1,244 TFLOP/s, 74 % of the library's
+// matrix products in a burst, 89 % of their sustained rate); 3 us at the
+// start, in which a CTA finds its share, and 2 to 5 us a block for what does
+// not overlap -- queries, first scores, output -- bound short calls (one token
+// over 333 keys: 12 us).
 //
 // The accumulator is rescaled only when a row's maximum has risen by more
 // than 2^8 since the reference that its weights were taken against: until
@@ -152,7 +167,9 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
-constexpr uint32_t kWholeTiles = 6;                     // blocks up to this long are not split when there is a CTA for each
+// Blocks up to this many tiles long are not split when there is a CTA for each
+// (one token over 333 keys, three tiles: 12.0 us, split and joined 13.4).
+constexpr uint32_t kWholeTiles = 6;
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
 template <int D, int kM>
@@ -258,9 +275,12 @@ __device__ __forceinline__ uint32_t block_count(const TensorArgs &p, const Reque
 }
 
 // What a block costs beside its tiles (queries, first scores, output), in
-// tiles: the units of a block begin with as many that hold no tile.
-template <int kM>
-constexpr uint32_t kBlockUnits = kM == 1 ? 1 : 3;
+// tiles: the units of a block begin with as many that hold no tile.  Fitted
+// to the times of CTAs with blocks of 1 to 40 tiles: 3.4 us beside 1.6 us a
+// tile (two row tiles, 64 channels), 5.2 beside 1.8 (128 channels), 0.7 beside
+// 2.6 (one row tile, where reading the keys is what takes the time).
+template <int D, int kM>
+constexpr uint32_t kBlockUnits = kM == 1 ? 0 : D == 64 ? 2 : 3;
 
 // Where a CTA stands in the order of units.
 struct Cursor {
@@ -276,40 +296,40 @@ struct Piece {
     Request q;
 };
 
-template <int kM>
+template <int D, int kM>
 __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece &w) {
     do {
-    if (c.left == 0) return false;
-    int32_t lo, hi;
-    block_tiles<kM>(p, c.q, c.block, &lo, &hi);
-    w.r = c.r;
-    w.head = c.head;
-    w.block = c.block;
-    w.q = c.q;
-    if (c.whole) {
-        w.t0 = lo;
-        w.t1 = hi;
-        c.left -= 1;
-    } else {
-        const uint32_t end = c.off + (uint32_t)umin64((uint32_t)(hi - lo) + kBlockUnits<kM> - c.off, c.left);
-        w.t0 = lo + max((int32_t)(c.off - kBlockUnits<kM>), 0);
-        w.t1 = lo + max((int32_t)(end - kBlockUnits<kM>), 0);
-        c.left -= end - c.off;
-    }
-    w.starts = w.t0 == lo;
-    w.ends = w.t1 == hi;
-    c.off = 0;
-    if (++c.block >= block_count<kM>(p, c.q)) {
-        c.block = 0;
-        if (++c.head >= p.kv.heads) {
-            c.head = 0;
-            while (c.left > 0 && ++c.r < p.kv.n_reqs) {
-                c.q = load_request(p.kv, c.r);
-                if (c.q.n > 0) break;
-            }
-            if (c.r >= p.kv.n_reqs) c.left = 0;
+        if (c.left == 0) return false;
+        int32_t lo, hi;
+        block_tiles<kM>(p, c.q, c.block, &lo, &hi);
+        w.r = c.r;
+        w.head = c.head;
+        w.block = c.block;
+        w.q = c.q;
+        if (c.whole) {
+            w.t0 = lo;
+            w.t1 = hi;
+            c.left -= 1;
+        } else {
+            const uint32_t end = c.off + (uint32_t)umin64((uint32_t)(hi - lo) + kBlockUnits<D, kM> - c.off, c.left);
+            w.t0 = lo + max((int32_t)(c.off - kBlockUnits<D, kM>), 0);
+            w.t1 = lo + max((int32_t)(end - kBlockUnits<D, kM>), 0);
+            c.left -= end - c.off;
         }
-    }
+        w.starts = w.t0 == lo;
+        w.ends = w.t1 == hi;
+        c.off = 0;
+        if (++c.block >= block_count<kM>(p, c.q)) {
+            c.block = 0;
+            if (++c.head >= p.kv.heads) {
+                c.head = 0;
+                while (c.left > 0 && ++c.r < p.kv.n_reqs) {
+                    c.q = load_request(p.kv, c.r);
+                    if (c.q.n > 0) break;
+                }
+                if (c.r >= p.kv.n_reqs) c.left = 0;
+            }
+        }
     } while (w.t0 == w.t1);  // a share may end in a block's first units, before its first tile
     return true;
 }
@@ -336,7 +356,7 @@ __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
 // Request r (none past the end) and its key tiles per KV head, a request per
 // lane of one warp: those of a few blocks are summed by their lane, larger
 // ones by all.  `most` grows to the tiles of the longest block.
-template <int kM>
+template <int D, int kM>
 __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, Request &q, uint32_t &most) {
     q.q0 = q.n = q.kv = 0;
     q.status = SZ_OK;
@@ -347,7 +367,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
     if (blocks <= 4)
         for (uint32_t b = 0; b < blocks; ++b) {
             block_tiles<kM>(p, q, b, &lo, &hi);
-            units += (uint32_t)(hi - lo) + kBlockUnits<kM>;
+            units += (uint32_t)(hi - lo) + kBlockUnits<D, kM>;
             most = max(most, (uint32_t)(hi - lo));
         }
     uint32_t many = __ballot_sync(0xFFFFFFFFu, blocks > 4);
@@ -362,7 +382,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
         uint64_t sum = 0;
         for (uint32_t b = lane; b < n; b += 32) {
             block_tiles<kM>(p, x, b, &lo, &hi);
-            sum += (uint32_t)(hi - lo) + kBlockUnits<kM>;
+            sum += (uint32_t)(hi - lo) + kBlockUnits<D, kM>;
             most = max(most, (uint32_t)(hi - lo));
         }
         sum = warp_sum(sum);
@@ -387,16 +407,16 @@ struct PlanScratch {
 };
 
 // This CTA's share of the units, found by all of its threads.
-template <int kM, int kThreads>
+template <int D, int kM>
 __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
-    constexpr uint32_t kW = kThreads / 32;
+    constexpr uint32_t kW = Shape<D, kM>::kThreads / 32;
     const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const uint32_t rounds = (p.kv.n_reqs + 32 * kW - 1) / (32 * kW);
     uint64_t mine = 0, per_head = 0, blocks = 0;
     uint32_t most = 0;
     Request q;
     for (uint32_t i = 0; i < rounds; ++i) {
-        per_head = lane_units<kM>(p, (wid * rounds + i) * 32 + lane, lane, q, most);
+        per_head = lane_units<D, kM>(p, (wid * rounds + i) * 32 + lane, lane, q, most);
         mine += per_head;
         blocks += block_count<kM>(p, q);
     }
@@ -436,7 +456,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
         uint64_t rem = u0 - before;
         for (uint32_t i = 0; i < rounds; ++i) {
             const uint32_t r0 = (wid * rounds + i) * 32;
-            if (rounds > 1) per_head = lane_units<kM>(p, r0 + lane, lane, q, most);
+            if (rounds > 1) per_head = lane_units<D, kM>(p, r0 + lane, lane, q, most);
             const uint64_t units = whole ? block_count<kM>(p, q) : per_head;
             const uint64_t end = warp_scan(units * p.kv.heads, lane);
             const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rem < end);
@@ -459,7 +479,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
                 if (b0 + lane < block_count<kM>(p, own)) {
                     int32_t lo, hi;
                     block_tiles<kM>(p, own, b0 + lane, &lo, &hi);
-                    n = whole ? 1u : (uint32_t)(hi - lo) + kBlockUnits<kM>;
+                    n = whole ? 1u : (uint32_t)(hi - lo) + kBlockUnits<D, kM>;
                 }
                 const uint64_t stop = warp_scan(n, lane);
                 const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < stop);
@@ -690,11 +710,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring0 + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0) : "memory");
         }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    find_share<kM, S::kThreads>(p, plan, control.scratch);  // synchronises the block
+    find_share<D, kM>(p, plan, control.scratch);  // synchronises the block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    allow_dependents();
+    if (p.rec) allow_dependents();  // the join, which waits; another kernel might read `out` too early
     const uint32_t tmem = same(control.tmem);
     Cursor cur;
     cur.r = plan.r;
@@ -721,7 +741,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         bool ok = true;
         SplitRec rec;
         rec.last = 0;
-        while (ok && next_piece<kM>(p, cur, w)) {
+        while (ok && next_piece<D, kM>(p, cur, w)) {
             if (w.starts && !w.ends) {
                 int32_t lo, hi;
                 block_tiles<kM>(p, w.q, w.block, &lo, &hi);
@@ -811,7 +831,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             }
         };
         for (uint32_t piece = 0; same(*fail) == 0; ++piece) {
-            if (same(next_piece<kM>(p, cur, w) ? 1u : 0u) == 0) break;
+            if (same(next_piece<D, kM>(p, cur, w) ? 1u : 0u) == 0) break;
             const int32_t t_begin = (int32_t)same((uint32_t)w.t0), t_end = (int32_t)same((uint32_t)w.t1), kv = (int32_t)same((uint32_t)w.q.kv);
             const uint32_t tiles = same(kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens ? 1u : 2u);  // row tiles in use
             const uint32_t buf = piece % S::kQueries;
@@ -907,7 +927,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         float *const swap_mine = &control.swap[half][S::kPaired ? row : 0], *const swap_other = &control.swap[half ^ 1][S::kPaired ? row : 0];
         const uint32_t my_token = row / p.group, my_head = row % p.group;
         uint32_t n = 0;  // tiles done by this row tile
-        while (next_piece<kM>(p, cur, w)) {
+        while (next_piece<D, kM>(p, cur, w)) {
             const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
             if ((uint32_t)w.q.n <= first) continue;
             const uint32_t rows = umin32((uint32_t)w.q.n - first, p.tile_tokens) * p.group;
@@ -1101,8 +1121,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 __threadfence();  // a CTA that fails sets timed_out, then the statuses
                 if (*(volatile unsigned long long *)p.timed_out == p.call) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
             }
-    }
         }
+    }
     // ------------------------------------------------------------------ end
     __syncthreads();
     if (failed) {  // rows may be unfinished: no result of this call stands
@@ -1122,7 +1142,9 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
 // out: a block of threads per CTA that began a split block, row tile and
 // D/8 channels; a thread holds one row's and, where rows are few (a decode
 // step, whose parts are many), one slice of the parts.  Slices and parts are
-// added in a fixed order.
+// added in a fixed order.  It takes 4 to 8 us behind the kernel above, its
+// launch overlapped; joining in the last CTA to arrive, behind a counter and
+// fences, took longer.
 constexpr int kJoinThreads = 128;
 constexpr uint32_t kJoinGroups = 8;
 
@@ -1338,7 +1360,11 @@ static cudaError_t launch_attention_t(const sz_paged_kv &kv, const sz_attention_
     if (!tensor_shape(kv, a)) return launch_any_t<T>(kv, a, status, s);
     // Two row tiles per CTA share a key tile; with no more rows per request
     // than one short tile holds (on average: the lengths are on the device),
-    // two CTAs per SM of one row tile each keep more copies in flight.
+    // two CTAs per SM of one row tile each keep more copies in flight.  Both
+    // ways, one and two row tiles: 64 requests of one token 129 and 149 us,
+    // one token over 131,071 keys 93 and 105, 8 requests of 5 tokens and 8
+    // heads 45 and 50; a 4,096 x 32,768 chunk 3.56 and 1.66 ms, ragged
+    // prompts 127 and 63 us, a 2,048-token chunk behind a window 504 and 266.
     const uint64_t group = a.q_heads / kv.heads, rows = kv.n_tokens * group;
     const bool two = rows > (uint64_t)kv.n_reqs * 64 || group > 64;
     if (kv.head_dim == 128)

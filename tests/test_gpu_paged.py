@@ -344,6 +344,24 @@ def test_captured_calls_follow_their_lengths():
         check(replayed, want[0], want[2])
 
 
+def test_the_output_is_encoded_behind_the_call():
+    # the one-pass encode reads its input before the kernel ahead of it has
+    # ended, unless that kernel holds it back
+    b = Batch([1] * 20, [300] * 20, 32, 8, 128, 16, BF16, seed=9)
+    k, v, table, q_begin, kv_len = b.cache()
+    q = b.q.to(DEV)
+    out = torch.zeros_like(q)
+    book = torch.arange(112, 128, dtype=torch.uint8, device=DEV)
+    want, _, _ = sz.paged_attention(q, k, v, table, q_begin, kv_len)
+    for _ in range(20):
+        out.zero_()
+        sz.paged_attention(q, k, v, table, q_begin, kv_len, out=out)
+        blob, _, status = sz.encode_one_pass(out, book)
+        back, st = sz.decode(blob, out.numel())
+        assert int(status) == 0 and int(st) == 0
+        assert torch.equal(back.view(-1), want.view(torch.int16).view(-1))
+
+
 def test_two_captured_calls_share_a_workspace():
     b = Batch([1, 2], [3000, 700], 8, 2, 128, 16, BF16)
     c = Batch([200], [900], 8, 2, 128, 16, BF16, seed=9)
