@@ -8,11 +8,18 @@
 // channels that are four whole pairs -- R/2 channels apart, or side by side
 // when pairs are adjacent -- so that turning needs no exchange between lanes.
 //
-// Bound: memory.  Every value is read once and written once, 4 bytes each.
+// Bound: memory.  Every value is read once and written once, 4 bytes each:
+// 4,096 tokens of 32 + 8 + 8 heads of 128 with norms take 21.8 us, 4.6 TB/s
+// (70 % of a copy; 4 us of them a launch of little work takes as well), 4,096
+// of 64 + 8 + 8 heads 33.6 us, 5.0 TB/s (76 %), one token for each of 64
+// requests 4.2 us, which is latency.  With counts, 2,500 tokens on average of
+// 3 requests, 8 + 8 heads, 17.9 us: an atomic in shared memory per value
+// bounds it.
 // A warp takes one token and a run of its heads (D = 128: two heads at a
 // time, two 8-byte loads per lane), kBatch heads' loads under way per lane;
-// nothing but the counts needs other warps.  The first loads are issued before the token's
-// request, page and angles are looked up, which is a chain of dependent loads.
+// nothing but the counts needs other warps.  The first loads are issued before
+// the token's request, page and angles are looked up, which is a chain of
+// dependent loads.
 // A token's angles are computed once per warp (a double product, reduced by
 // whole turns in double so that a position of millions keeps its angle, then
 // a 32-bit sine and cosine) and serve all of its heads.
@@ -26,7 +33,10 @@ namespace sz {
 // SMs; with counts as many threads as bins.
 constexpr int kAppendWarps = 4, kCountWarps = 8;
 constexpr uint32_t kMaxHeadDim = 256;
-constexpr int kBatch = 4;  // head groups whose loads a warp has under way
+// Blocks per SM that the registers allow: without counts 72 registers and
+// nearly no spills for 7 (6 or 8 blocks took 4 to 25 % longer on chunks), with
+// counts 3 with their 32 KB of columns each.
+constexpr int kAppendBlocks = 7, kCountBlocks = 3;
 
 struct AppendArgs {
     sz_paged_kv kv;
@@ -122,6 +132,10 @@ template <typename T, int kLanes, bool kAdjacent, bool kCount>
 __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token, uint32_t h_begin, uint32_t h_end, uint32_t lane,
                                              float2 *cs, uint32_t column, uint32_t known_r, const Request &known) {
     constexpr uint32_t kHeads = 32 / kLanes;  // at a time
+    // Head groups whose loads a warp has under way: two where many warps run
+    // (with four a decode step took 4.7 us instead of 4.3), four next to the
+    // counts' 24 warps per SM (17.9 us, with two 19.1).
+    constexpr int kBatch = kCount ? 4 : 2;
     const sz_paged_kv &kv = p.kv;
     const sz_append_args &a = p.a;
     const uint32_t D = kv.head_dim, l = lane % kLanes, group = lane / kLanes;
@@ -257,7 +271,7 @@ __device__ __forceinline__ void append_token(const AppendArgs &p, uint32_t token
 }
 
 template <typename T, int kLanes, bool kAdjacent, bool kCount>
-__global__ void __launch_bounds__(32 * (kCount ? kCountWarps : kAppendWarps), kCount ? 3 : 8) append_kernel(const __grid_constant__ AppendArgs p) {
+__global__ void __launch_bounds__(32 * (kCount ? kCountWarps : kAppendWarps), kCount ? kCountBlocks : kAppendBlocks) append_kernel(const __grid_constant__ AppendArgs p) {
     constexpr uint32_t kWarps = kCount ? kCountWarps : kAppendWarps, kThreads = 32 * kWarps;
     __shared__ float2 cs[kWarps][kMaxHeadDim / 2];
     __shared__ uint32_t columns[kCount ? 256 * 32 : 1];
@@ -339,19 +353,30 @@ static cudaError_t launch_append_lanes(AppendArgs &p, int sms, cudaStream_t s) {
     const uint64_t tokens = p.kv.n_tokens;
     if (p.a.d_hists_or_null) {
         // Counts cost a pass over 32 KB of shared memory per block and request:
-        // as many blocks as run at once (three per SM, half of them keys and
-        // half values), of at least a token per warp.
-        const uint64_t want = umax64(1, (uint64_t)sms * 3 / 2);
+        // as many blocks as run at once (half of them keys and half values), of
+        // at least a token per warp.  (17.9 us; with two thirds or twice as
+        // many blocks 19.7 and 20.1.)
+        const uint64_t want = umax64(1, (uint64_t)sms * kCountBlocks / 2);
         p.tokens_per_block = (uint32_t)umax64(kCountWarps, div_up(tokens, want));
         const dim3 grid((uint32_t)umax64(1, div_up(tokens, p.tokens_per_block)), p.a.q_heads ? 3 : 2);
         append_kernel<T, kLanes, kAdjacent, true><<<grid, 32 * kCountWarps, 0, s>>>(p);
         return cudaGetLastError();
     }
-    // A warp takes a token's heads in slices: as many warps as keep the SMs
-    // busy (24 each), and no more, since each looks its token up anew.
-    const uint64_t groups = div_up(heads, at_once);
-    const uint64_t per_warp = umax64(div_up(groups, 65535), tokens * groups / ((uint64_t)sms * 24));
-    p.slice_heads = (uint32_t)umin64(groups, per_warp) * at_once;
+    // A warp takes a token's heads in slices.  Each slice looks its token up
+    // anew, which costs about as much as four groups of heads, and blocks run
+    // in waves of kAppendBlocks per SM: the number of slices with the least
+    // waves x (groups + 4).  (Always as many slices as give 24 warps per SM:
+    // 4,096 tokens of 48 heads 22.3 us against 21.8.)
+    const uint64_t groups = div_up(heads, at_once), blocks = umax64(1, div_up(tokens, kAppendWarps));
+    uint64_t best = ~0ull;
+    for (uint64_t slices = div_up(groups, 65535); slices <= groups; slices += 1 + slices / 8) {
+        const uint64_t each = div_up(groups, slices);
+        const uint64_t cost = div_up(blocks * div_up(groups, each), (uint64_t)sms * kAppendBlocks) * (each + 4);
+        if (cost < best) {
+            best = cost;
+            p.slice_heads = (uint32_t)each * at_once;
+        }
+    }
     p.tokens_per_block = kAppendWarps;
     const dim3 grid((uint32_t)umax64(1, div_up(tokens, kAppendWarps)), (uint32_t)div_up(heads, p.slice_heads));
     append_kernel<T, kLanes, kAdjacent, false><<<grid, 32 * kAppendWarps, 0, s>>>(p);
