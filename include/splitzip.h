@@ -429,11 +429,14 @@ sz_status sz_select_codebook_batched(uint32_t n_hists, const uint32_t *d_hists, 
  *   dtype           SZ_BF16 or SZ_FP16 (of the pools and of q, k, v and out)
  *   d_page_table    int32: request r's i-th page is page
  *                   d_page_table[r*table_stride + i], i < max_pages.  Entries
- *                   behind a request's last token are not read.
+ *                   behind a request's last token are not read, nor by the
+ *                   attention those before its first query's window.
  *   d_q_begin       int32[n_reqs + 1]: request r's new tokens are rows
  *                   d_q_begin[r] .. d_q_begin[r+1] of q, k, v and out
  *                   (ascending, the last at most n_tokens).  Rows outside
- *                   every request are left alone.
+ *                   every request are left alone.  Padding rows can be
+ *                   requests with kv_len 0: nothing is cached for them
+ *                   (the append gives SZ_ERR_INVALID), their attention is 0.
  *   d_kv_len        int32[n_reqs]: tokens cached once the new ones are in;
  *                   new token i of n sits at position kv_len - n + i
  *   n_tokens        rows of q, k, v and out
@@ -442,8 +445,9 @@ sz_status sz_select_codebook_batched(uint32_t n_hists, const uint32_t *d_hists, 
  * d_status (required) gets one status per request: SZ_ERR_INVALID for rows
  * out of order or out of range, a negative length or a page number outside
  * the pool, SZ_ERR_CAPACITY for a kv_len above max_pages*page_tokens.  The
- * results of a request whose status is not SZ_OK must not be used; nothing
- * outside the caller's buffers is touched for it.
+ * results of a request whose status is not SZ_OK must not be used, and where
+ * q_begin is out of order those of no request; nothing outside the caller's
+ * buffers is touched either way.  At most 2^30 rows, requests and positions.
  */
 #define SZ_BF16 1u
 #define SZ_FP16 2u
@@ -495,7 +499,8 @@ typedef struct sz_paged_kv {
  *                   r's keys go to row d_hist_rows[r], its values to row
  *                   d_hist_rows[n_reqs + r]; without d_hist_rows to rows r
  *                   and n_reqs + r.  A row at or above n_hists gives
- *                   SZ_ERR_INVALID.
+ *                   SZ_ERR_INVALID.  Only what this call writes is counted:
+ *                   a token written twice counts twice.
  * A request with more new tokens than kv_len gives SZ_ERR_INVALID.  The pages
  * written must belong to one request each.  Norm, angle and rotation are
  * computed in 32 bits (the angle's product and its reduction in 64) and
@@ -547,7 +552,14 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *args, int32_
  * whatever bits they hold.  Scores, sums and the running maximum are 32-bit;
  * the weights exp(s - m) are rounded to the 16-bit type before they meet the
  * values.  The result does not depend on timing: parts of a split row are
- * joined in a fixed order.
+ * joined in a fixed order.  A key or value hidden from a query does not reach
+ * it either, whatever its bits.
+ * Heads of 64 or 128 channels run on the tensor cores, if pages hold a
+ * multiple of 8 tokens (of 128 above 128), at most 128 query heads share a KV
+ * head and scale is positive; other shapes are computed key by key.
+ * A device-side wait that runs out sets every status of the call to
+ * SZ_ERR_DEVICE_TIMEOUT.  The workspace remembers the call: replays of a
+ * captured call report it until the workspace is overwritten.
  */
 typedef struct sz_attention_args {
     const void *d_q;
@@ -597,7 +609,7 @@ sz_status sz_encode_static(const uint16_t *d_in, uint64_t n, uint8_t *d_out, uin
 /*
  * sz_set_wait_limit_ns -- upper bound, in nanoseconds of device time, of
  * every device-side wait of every entry point (a pipeline stage of the
- * encode or decode kernel waiting for its bulk copy).
+ * encode, decode or attention kernel waiting for its bulk copy or products).
  * Default 1e9 (one second).  A wait that runs out sets
  * SZ_ERR_DEVICE_TIMEOUT in the segment's status and the kernel returns.
  * Applies to calls made after it, process-wide.
@@ -605,8 +617,8 @@ sz_status sz_encode_static(const uint16_t *d_in, uint64_t n, uint8_t *d_out, uin
 sz_status sz_set_wait_limit_ns(uint64_t limit_ns);
 
 /*
- * sz_debug_set_flags -- test hook.  Bit 0: the encode and decode kernels'
- * copy threads issue no bulk copy, so every stage wait of their consumer
+ * sz_debug_set_flags -- test hook.  Bit 0: the encode, decode and
+ * attention kernels' copy threads issue no bulk copy, so every stage wait of their consumer
  * threads runs out (exercises the timeout path without faulting
  * anything).  Bit 1: the decode kernel's copy thread publishes the values
  * part of its stages but never their escape part, so the consumers' wait

@@ -27,7 +27,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // loads and the exchanges between lanes, and every row reads its keys anew:
 // it is there for the shapes that the tensor-core kernel does not take.
 // (Both on the same calls: one token over 333 keys 28 us, there 12; 5 tokens
-// of 8 requests over thousands of keys 1,680 and 45 us; ragged prompts 3,370
+// of 16 requests over thousands of keys 1,680 and 45 us; ragged prompts 3,370
 // and 63 us.)
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(kGeneralThreads) attention_any_kernel(sz_paged_kv kv, sz_attention_args a, int32_t *status) {
@@ -1271,6 +1271,19 @@ static bool make_map(CUtensorMap *map, uint32_t dtype, void *base, int rank, con
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Let `Kernel` use `bytes` of dynamic shared memory, asked once per device.
+template <auto Kernel>
+static cudaError_t allow_shared(uint32_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (const cudaError_t e = cudaGetDevice(&dev)) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Which shapes the tensor-core kernel takes: heads of 64 or 128 channels, a
 // positive scale (the running maximum is of unscaled scores), row tiles that
 // hold a whole group, and pages whose copies start on a swizzle group of 8
@@ -1362,7 +1375,7 @@ static cudaError_t launch_attention_t(const sz_paged_kv &kv, const sz_attention_
     // than one short tile holds (on average: the lengths are on the device),
     // two CTAs per SM of one row tile each keep more copies in flight.  Both
     // ways, one and two row tiles: 64 requests of one token 129 and 149 us,
-    // one token over 131,071 keys 93 and 105, 8 requests of 5 tokens and 8
+    // one token over 131,071 keys 93 and 105, 16 requests of 5 tokens and 8
     // heads 45 and 50; a 4,096 x 32,768 chunk 3.56 and 1.66 ms, ragged
     // prompts 127 and 63 us, a 2,048-token chunk behind a window 504 and 266.
     const uint64_t group = a.q_heads / kv.heads, rows = kv.n_tokens * group;

@@ -333,19 +333,6 @@ void prefer_max_shared() {
         (void)cudaGetLastError();
 }
 
-// Let `Kernel` use `bytes` of dynamic shared memory, asked once per device.
-template <auto Kernel>
-cudaError_t allow_shared(uint32_t bytes) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    if (const cudaError_t e = cudaGetDevice(&dev)) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 template <typename... Params, typename... Args>
 cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                          Args &&...args) {

@@ -15,7 +15,8 @@ Pages of a contiguous [page, head, token, channel] pool are pages of
 
 Both calls run on the current stream of the tensors' device, or on ``stream``
 (their new tensors are then allocated on it), never synchronise, and return a
-status tensor with one word per request.  Neither has a gradient.
+status tensor with one word per request.  Neither has a gradient: where
+gradients are recorded, tensors that require one are refused.
 """
 from __future__ import annotations
 
