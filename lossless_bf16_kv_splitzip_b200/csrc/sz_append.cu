@@ -12,7 +12,7 @@
 // 4,096 tokens of 32 + 8 + 8 heads of 128 with norms take 21.8 us, 4.6 TB/s
 // (70 % of a copy; 4 us of them a launch of little work takes as well), 4,096
 // of 64 + 8 + 8 heads 33.6 us, 5.0 TB/s (76 %), one token for each of 64
-// requests 4.2 us, which is latency.  With counts, 2,500 tokens on average of
+// requests 4.5 us, which is latency.  With counts, 2,500 tokens on average of
 // 3 requests, 8 + 8 heads, 17.9 us: an atomic in shared memory per value
 // bounds it.
 // A warp takes one token and a run of its heads (D = 128: two heads at a

@@ -22,26 +22,29 @@ from __future__ import annotations
 
 import functools
 import math
+import threading
 
 _BINDING = None
+_LOADING = threading.Lock()
 
 
 def binding():
     """The compiled part (csrc/sz_binding.cpp), which checks the arguments,
     allocates the results and calls the library; built in-tree if missing."""
     global _BINDING
-    if _BINDING is None:
-        import ctypes
+    with _LOADING:
+        if _BINDING is None:
+            import ctypes
 
-        import torch  # noqa: F401  its libraries come first
+            import torch  # noqa: F401  its libraries come first
 
-        from . import lib
-        from ._build import build_binding
-        build_binding()
-        from . import _binding
-        loaded = lib()
-        _binding.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (loaded.sz_append_kv, loaded.sz_paged_attention)))
-        _BINDING = _binding
+            from . import lib
+            from ._build import build_binding
+            build_binding()
+            from . import _binding
+            loaded = lib()
+            _binding.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (loaded.sz_append_kv, loaded.sz_paged_attention)))
+            _BINDING = _binding
     return _BINDING
 
 

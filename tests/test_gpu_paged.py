@@ -312,6 +312,29 @@ def test_attention_repeats_bit_for_bit_and_on_two_streams():
         assert torch.equal(o, first)
 
 
+def test_two_host_threads_call_at_once():
+    from concurrent.futures import ThreadPoolExecutor
+    batches = [Batch([3, 40], [300, 700], 8, 2, 128, 16, BF16, seed=11), Batch([1, 1, 1], [2000, 5, 90], 16, 4, 64, 32, FP16, seed=12)]
+    given = [(b.q.to(DEV), *b.cache()) for b in batches]
+    alone = [sz.paged_attention(*x)[0].clone() for x in given]
+    torch.cuda.synchronize()
+
+    def work(x, want):
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            out, _, status = sz.paged_attention(*x, stream=s)
+            rows = x[0][:, : x[1].shape[1]].contiguous()
+            pages = [t.clone() for t in x[1:3]]
+            s.wait_stream(torch.cuda.current_stream())
+            _, put = sz.append_kv(rows, rows, *pages, *x[3:], stream=s)
+            s.synchronize()
+            assert torch.equal(out, want) and not status.any() and not put.any()
+
+    with ThreadPoolExecutor(2) as pool:
+        for f in [pool.submit(work, x, want) for x, want in zip(given, alone)]:
+            f.result()
+
+
 def test_captured_calls_follow_their_lengths():
     b = Batch([1, 1, 2], [600, 40, 90], 8, 2, 128, 16, FP16, width=64)
     k, v, table, q_begin, kv_len = b.cache()
