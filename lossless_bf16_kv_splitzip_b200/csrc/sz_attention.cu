@@ -334,21 +334,28 @@ __device__ __forceinline__ bool next_piece(const TensorArgs &p, Cursor &c, Piece
     return true;
 }
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+// Sums of units, in 32 bits (U) where the call's sizes say that they fit, which
+// takes half the instructions: 0.4 us of every call (one token over 333 keys
+// 11.8 us, in 64 bits 12.2; both in one kernel, chosen there, gain nothing,
+// since it is the fetching of new instructions that takes the time).
+template <typename U>
+__device__ __forceinline__ U warp_sum(U v) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     return v;
 }
-__device__ __forceinline__ uint64_t warp_scan(uint64_t v, uint32_t lane) {  // inclusive
+template <typename U>
+__device__ __forceinline__ U warp_scan(U v, uint32_t lane) {  // inclusive
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        const U y = __shfl_up_sync(0xFFFFFFFFu, v, d);
         if (lane >= (uint32_t)d) v += y;
     }
     return v;
 }
 
 // Quotient of numbers that mostly fit 32 bits.
+__device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b) { return a / b; }
 __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
     return ((a | b) >> 32) == 0 ? (uint32_t)a / (uint32_t)b : a / b;
 }
@@ -356,13 +363,13 @@ __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
 // Request r (none past the end) and its key tiles per KV head, a request per
 // lane of one warp: those of a few blocks are summed by their lane, larger
 // ones by all.  `most` grows to the tiles of the longest block.
-template <int D, int kM>
-__device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, Request &q, uint32_t &most) {
+template <typename U, int D, int kM>
+__device__ U lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, Request &q, uint32_t &most) {
     q.q0 = q.n = q.kv = 0;
     q.status = SZ_OK;
     if (r < p.kv.n_reqs) q = load_request(p.kv, r);
     const uint32_t blocks = block_count<kM>(p, q);
-    uint64_t units = 0;
+    U units = 0;
     int32_t lo, hi;
     if (blocks <= 4)
         for (uint32_t b = 0; b < blocks; ++b) {
@@ -379,7 +386,7 @@ __device__ uint64_t lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, R
         x.n = __shfl_sync(0xFFFFFFFFu, q.n, src);
         x.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
         const uint32_t n = block_count<kM>(p, x);
-        uint64_t sum = 0;
+        U sum = 0;
         for (uint32_t b = lane; b < n; b += 32) {
             block_tiles<kM>(p, x, b, &lo, &hi);
             sum += (uint32_t)(hi - lo) + kBlockUnits<D, kM>;
@@ -407,16 +414,16 @@ struct PlanScratch {
 };
 
 // This CTA's share of the units, found by all of its threads.
-template <int D, int kM>
+template <typename U, int D, int kM>
 __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
     constexpr uint32_t kW = Shape<D, kM>::kThreads / 32;
     const uint32_t lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const uint32_t rounds = (p.kv.n_reqs + 32 * kW - 1) / (32 * kW);
-    uint64_t mine = 0, per_head = 0, blocks = 0;
+    U mine = 0, per_head = 0, blocks = 0;
     uint32_t most = 0;
     Request q;
     for (uint32_t i = 0; i < rounds; ++i) {
-        per_head = lane_units<D, kM>(p, (wid * rounds + i) * 32 + lane, lane, q, most);
+        per_head = lane_units<U, D, kM>(p, (wid * rounds + i) * 32 + lane, lane, q, most);
         mine += per_head;
         blocks += block_count<kM>(p, q);
     }
@@ -429,11 +436,11 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
         x.most[wid] = most;
     }
     __syncthreads();
-    uint64_t total = 0, before = 0, total_blocks = 0, before_blocks = 0;
+    U total = 0, before = 0, total_blocks = 0, before_blocks = 0;
     for (uint32_t w = 0; w < kW; ++w) {
-        if (w < wid) before += x.units[w], before_blocks += x.blocks[w];
-        total += x.units[w];
-        total_blocks += x.blocks[w];
+        if (w < wid) before += (U)x.units[w], before_blocks += (U)x.blocks[w];
+        total += (U)x.units[w];
+        total_blocks += (U)x.blocks[w];
         most = max(most, x.most[w]);
     }
     // A few short blocks: one CTA each, which costs less than joining parts.
@@ -441,31 +448,31 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
     if (whole) total = total_blocks, before = before_blocks, mine = blocks;
     // Every CTA that works has at least one unit, so that the parts of a block
     // are those of consecutive CTAs.
-    const uint32_t used = (uint32_t)umin64(p.ctas, umax64(1, total));
+    const U used = total < p.ctas ? (total > 0 ? total : 1) : p.ctas;
     const bool works = blockIdx.x < used;
-    const uint64_t u0 = works ? divide(blockIdx.x * total, used) : 0, u1 = works ? divide((blockIdx.x + 1) * total, used) : 0;
+    const U u0 = works ? divide(blockIdx.x * total, used) : 0, u1 = works ? divide((blockIdx.x + 1) * total, used) : 0;
     if (threadIdx.x == 0) {
         s.left = 0;
         s.first = u0;
         s.total = total;
-        s.used = used;
+        s.used = (uint32_t)used;
         s.whole = whole;
     }
     __syncthreads();
     if (u1 > u0 && u0 >= before && u0 < before + mine) {  // one warp
-        uint64_t rem = u0 - before;
+        U rem = u0 - before;
         for (uint32_t i = 0; i < rounds; ++i) {
             const uint32_t r0 = (wid * rounds + i) * 32;
-            if (rounds > 1) per_head = lane_units<D, kM>(p, r0 + lane, lane, q, most);
-            const uint64_t units = whole ? block_count<kM>(p, q) : per_head;
-            const uint64_t end = warp_scan(units * p.kv.heads, lane);
+            if (rounds > 1) per_head = lane_units<U, D, kM>(p, r0 + lane, lane, q, most);
+            const U units = whole ? block_count<kM>(p, q) : per_head;
+            const U end = warp_scan<U>(units * p.kv.heads, lane);
             const uint32_t hit = __ballot_sync(0xFFFFFFFFu, rem < end);
             if (hit == 0) {
                 rem -= __shfl_sync(0xFFFFFFFFu, end, 31);
                 continue;
             }
             const int src = __ffs(hit) - 1;
-            const uint64_t w = __shfl_sync(0xFFFFFFFFu, units, src);
+            const U w = __shfl_sync(0xFFFFFFFFu, units, src);
             rem -= __shfl_sync(0xFFFFFFFFu, end - units * p.kv.heads, src);
             const uint32_t head = (uint32_t)divide(rem, w);
             rem -= head * w;
@@ -475,13 +482,13 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
             own.kv = __shfl_sync(0xFFFFFFFFu, q.kv, src);
             own.status = SZ_OK;
             for (uint32_t b0 = 0; b0 < block_count<kM>(p, own); b0 += 32) {
-                uint64_t n = 0;
+                U n = 0;
                 if (b0 + lane < block_count<kM>(p, own)) {
                     int32_t lo, hi;
                     block_tiles<kM>(p, own, b0 + lane, &lo, &hi);
                     n = whole ? 1u : (uint32_t)(hi - lo) + kBlockUnits<D, kM>;
                 }
-                const uint64_t stop = warp_scan(n, lane);
+                const U stop = warp_scan<U>(n, lane);
                 const uint32_t here = __ballot_sync(0xFFFFFFFFu, rem < stop);
                 if (here == 0) {
                     rem -= __shfl_sync(0xFFFFFFFFu, stop, 31);
@@ -652,7 +659,7 @@ struct Control {  // behind the tiles in shared memory
     };
 };
 
-template <typename T, int D, int kM>
+template <typename T, int D, int kM, typename U>
 __global__ void __launch_bounds__(Shape<D, kM>::kThreads, Shape<D, kM>::kCtasPerSm)
 attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ CUtensorMap q_map,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -710,7 +717,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring0 + half * kHalfBytes + row * kRowBytes + piece * 16), "r"(0) : "memory");
         }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    find_share<D, kM>(p, plan, control.scratch);  // synchronises the block
+    find_share<U, D, kM>(p, plan, control.scratch);  // synchronises the block
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1345,6 +1352,8 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     // (find_share comes to the same), nothing needs joining.
     const uint64_t span = (uint64_t)S::kTiles * p.tile_tokens, blocks = kv.heads * (kv.n_reqs + kv.n_tokens / span);
     const bool split = blocks > p.ctas || div_up((uint64_t)kv.max_pages * kv.page_tokens, p.key_tile) > kWholeTiles;
+    const uint64_t most = div_up((uint64_t)kv.max_pages * kv.page_tokens, p.key_tile) + 1 + kBlockUnits<D, kM>;  // units of a block
+    const bool wide = blocks >= (1ull << 32) / (p.ctas + 1) / most;  // units times CTAs may pass 32 bits
     p.rec = split ? reinterpret_cast<SplitRec *>(at + 8) : nullptr;
     p.call = next_call();
     p.status = status;
@@ -1360,8 +1369,13 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     if (!encode_tiled() || !make_map(&q_map, kv.dtype, const_cast<void *>(a.d_q), 3, q_size, q_stride, q_box) ||
         !make_map(&k_map, kv.dtype, kv.d_k, 4, size, k_stride, box) || !make_map(&v_map, kv.dtype, kv.d_v, 4, size, v_stride, box))
         return cudaErrorInvalidValue;
-    if (const cudaError_t e = allow_shared<attention_kernel<T, D, kM>>(S::kSmem)) return e;
-    attention_kernel<T, D, kM><<<p.ctas, S::kThreads, S::kSmem, s>>>(p, q_map, k_map, v_map);
+    if (wide) {
+        if (const cudaError_t e = allow_shared<attention_kernel<T, D, kM, uint64_t>>(S::kSmem)) return e;
+        attention_kernel<T, D, kM, uint64_t><<<p.ctas, S::kThreads, S::kSmem, s>>>(p, q_map, k_map, v_map);
+    } else {
+        if (const cudaError_t e = allow_shared<attention_kernel<T, D, kM, uint32_t>>(S::kSmem)) return e;
+        attention_kernel<T, D, kM, uint32_t><<<p.ctas, S::kThreads, S::kSmem, s>>>(p, q_map, k_map, v_map);
+    }
     if (const cudaError_t e = cudaGetLastError()) return e;
     if (!split) return cudaSuccess;
     return launch_after(attention_join_kernel<T, D, kM>, dim3(p.ctas, kJoinGroups, kM), dim3(kJoinThreads), 0, s, p);

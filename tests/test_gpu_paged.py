@@ -116,6 +116,23 @@ def test_attention_of_a_long_chunk():
     attend_and_check(Batch([700, 90], [1500, 1203], 4, 1, 128, 16, BF16, seed=4))
 
 
+@pytest.mark.parametrize("new,kv", [([1, 1, 2], [40, 9001, 700]), ([300, 9], [555, 1400]), ([2, 0, 1] * 50, [90, 3, 1] * 50)], ids=str)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_page_tables_of_millions_of_columns(new, kv, dim):
+    # whose sizes no longer say that the shares can be counted in 32 bits
+    b = Batch(new, kv, 8, 8 if dim == 64 else 2, dim, 512, BF16, seed=21)
+    out = []
+    k, v, table, q_begin, kv_len = b.cache()
+    far = torch.full((len(kv), (1 << 21) // (1 if len(kv) < 4 else 32)), -1, dtype=torch.int32, device=DEV)
+    far[:, : table.shape[1]] = table
+    for t in (table, far):
+        out.append(sz.paged_attention(b.q.to(DEV), k, v, t, q_begin, kv_len, return_lse=True))
+        assert not out[-1][2].any()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    check(out[1][0], want[0], want[2])
+
+
 @pytest.mark.parametrize("dim,page", [(128, 16), (64, 64), (80, 16)])
 def test_more_new_tokens_than_cached(dim, page):
     # the first rows stand before the cache's beginning and see nothing
