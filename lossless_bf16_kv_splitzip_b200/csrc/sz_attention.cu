@@ -1040,7 +1040,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 *swap_mine = l;
                 pair_sync(pair);
                 l = half ? *swap_other + l : l + *swap_other;
-                pair_sync(pair);  // read by both before it is written again
             }
             bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
@@ -1110,6 +1109,14 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             *(uint4 *)(part + S::part_o(m_tile, half * (kOwn / 4) + i * 8 + j, row)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
                 if (half == 0 && row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
+            }
+            // Both of a pair have read their channels before either hands over
+            // weights of the next block, whose first product writes all
+            // channels once the first half's are there (a warp without rows
+            // there hands over at once); the exchanged sums are read as well.
+            if constexpr (S::kPaired) {
+                tc_fence_before();
+                pair_sync(pair);
             }
         }
         tc_fence_before();

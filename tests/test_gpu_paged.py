@@ -217,6 +217,32 @@ def test_values_hidden_from_a_row_do_not_reach_it(shape, value):
         check(out[new[0] - 1, :, same], want[0][new[0] - 1, :, same], want[2][new[0] - 1, :, same]) if not window else None
 
 
+@pytest.mark.parametrize("dim,hidden", [(128, None), (128, math.inf), (64, None), (64, math.nan)], ids=str)
+def test_short_blocks_behind_long_ones(dim, hidden):
+    # a CTA's blocks of 64 and of 8 rows in turn: a warp that holds rows of the
+    # first alone must not let the next block's products begin while the other
+    # warp of its rows still reads.  A value that is not finite, in the upper
+    # channels of a key that the rows before do not see, keeps that one longest.
+    b = Batch([8, 1] * 20, [1500, 1400] * 20, 64, 8, dim, 16, BF16, seed=31)
+    want = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    clean = torch.ones(b.rows, dtype=torch.bool)
+    k, v, table, q_begin, kv_len = b.cache()
+    if hidden is not None:
+        for r in range(0, len(b.kv), 2):
+            last = b.kv[r] - 1
+            v[int(b.table[r, last // 16]), :, last % 16, dim // 2 + 5] = hidden
+            clean[int(b.q_begin[r + 1]) - 1] = False  # the row that sees it
+    for _ in range(5):
+        out, lse, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, return_lse=True)
+        assert not status.any()
+        out = out.cpu()
+        check(out[clean], want[0][clean], want[2][clean])
+        check(lse, want[1], want[3])
+        seen = torch.arange(dim) != dim // 2 + 5
+        check(out[~clean][..., seen], want[0][~clean][..., seen], want[2][~clean][..., seen])
+        assert not torch.isfinite(out[~clean][..., dim // 2 + 5].float()).any()
+
+
 def test_waits_that_run_out_are_reported():
     # the copy warps issue nothing, so every wait ends by its limit
     few, many = Batch([1, 2], [3000, 70], 8, 2, 128, 16, BF16), Batch([300], [900], 8, 2, 64, 16, FP16)
