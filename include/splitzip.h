@@ -446,8 +446,9 @@ sz_status sz_select_codebook_batched(uint32_t n_hists, const uint32_t *d_hists, 
  * out of order or out of range, a negative length or a page number outside
  * the pool, SZ_ERR_CAPACITY for a kv_len above max_pages*page_tokens.  The
  * results of a request whose status is not SZ_OK must not be used, and where
- * q_begin is out of order those of no request; nothing outside the caller's
- * buffers is touched either way.  At most 2^30 rows, requests and positions.
+ * q_begin is out of order those of no request (the attention may then write no
+ * row at all); nothing outside the caller's buffers is touched either way.  At
+ * most 2^30 rows, requests and positions.
  */
 #define SZ_BF16 1u
 #define SZ_FP16 2u

@@ -362,12 +362,24 @@ __device__ __forceinline__ uint64_t divide(uint64_t a, uint64_t b) {
 
 // Request r (none past the end) and its key tiles per KV head, a request per
 // lane of one warp: those of a few blocks are summed by their lane, larger
-// ones by all.  `most` grows to the tiles of the longest block.
+// ones by all.  `most` grows to the tiles of the longest block, and to
+// kDisordered where a request ends before it begins: only rows in order share
+// the call's n_tokens, which bounds all sums of units (and the time that this
+// takes).
+constexpr uint32_t kDisordered = 0xFFFFFFFFu;
 template <typename U, int D, int kM>
 __device__ U lane_units(const TensorArgs &p, uint32_t r, uint32_t lane, Request &q, uint32_t &most) {
     q.q0 = q.n = q.kv = 0;
     q.status = SZ_OK;
-    if (r < p.kv.n_reqs) q = load_request(p.kv, r);
+    bool back = false;
+    if (r < p.kv.n_reqs) {
+        q = load_request(p.kv, r);
+        back = __ldg(p.kv.d_q_begin + r + 1) < q.q0;
+    }
+    if (__any_sync(0xFFFFFFFFu, back)) {
+        most = kDisordered;
+        return 0;
+    }
     const uint32_t blocks = block_count<kM>(p, q);
     U units = 0;
     int32_t lo, hi;
@@ -446,6 +458,7 @@ __device__ void find_share(const TensorArgs &p, PlanShared &s, PlanScratch &x) {
     // A few short blocks: one CTA each, which costs less than joining parts.
     const bool whole = total_blocks <= p.ctas && most <= kWholeTiles;
     if (whole) total = total_blocks, before = before_blocks, mine = blocks;
+    if (most == kDisordered) total = 0;  // the requests overlap: nothing is done, and the statuses say so
     // Every CTA that works has at least one unit, so that the parts of a block
     // are those of consecutive CTAs.
     const U used = total < p.ctas ? (total > 0 ? total : 1) : p.ctas;
@@ -1170,7 +1183,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
     const uint32_t tid = threadIdx.x, c0 = blockIdx.x, chunk = blockIdx.y * kChunks, m_tile = blockIdx.z;
     grid_dependency_wait();
     const SplitRec w = p.rec[c0];
-    if (w.last == 0) return;
+    if (w.last <= c0 || w.last >= p.ctas) return;
     const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
     if ((uint32_t)w.q.n <= first) return;
     const uint32_t rows = umin32((uint32_t)w.q.n - first, p.tile_tokens) * p.group, parts = w.last - c0 + 1;

@@ -343,6 +343,25 @@ def test_refused_requests(dim):
         assert call().cpu().tolist() == [0, sz.SZ_ERR_INVALID, 0, sz.SZ_ERR_INVALID, sz.SZ_ERR_INVALID]
 
 
+@pytest.mark.parametrize("reqs,rows,heads,kv_heads", [(32, 65536, 32, 8), (512, 4096, 32, 8), (512, 32768, 8, 8)])
+def test_requests_that_overlap_are_not_computed(reqs, rows, heads, kv_heads):
+    # q_begin goes back and forth, so that every second request claims all rows:
+    # far more work than n_tokens rows are, and more than 32-bit shares count
+    dim, page, kv = 64, 128, 32768
+    k = torch.zeros((4, kv_heads, page, dim), dtype=BF16, device=DEV)
+    table = torch.zeros((reqs, kv // page), dtype=torch.int32, device=DEV)
+    q = torch.zeros((rows, heads, dim), dtype=BF16, device=DEV)
+    out = torch.full_like(q, 7.0)
+    back = torch.tensor([0, rows] * (reqs // 2) + [0], dtype=torch.int32, device=DEV)
+    kv_len = torch.full((reqs,), kv, dtype=torch.int32, device=DEV)
+    need = sz.sz_plan_attention(dim)
+    buffer = torch.full((need + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
+    _, _, status = sz.paged_attention(q, k, k, table, back, kv_len, out=out, workspace=buffer[:need])
+    torch.cuda.synchronize()
+    assert status.cpu().tolist() == [0, sz.SZ_ERR_INVALID] * (reqs // 2)
+    assert bool((out == 7.0).all()) and bool((buffer[need:] == 77).all())
+
+
 def test_attention_repeats_bit_for_bit_and_on_two_streams():
     b = Batch([1, 3, 200], [5000, 700, 900], 8, 2, 128, 16, BF16)
     args = [b.q.to(DEV)] + b.cache()
