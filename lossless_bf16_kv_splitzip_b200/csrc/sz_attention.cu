@@ -1037,7 +1037,13 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                     }
                     sum = add2(sum, sum1);
                     tmem_wait_st();
-                } else if (kParts == 2 && lane == 0) {
+                } else if (S::kPaired) {
+                    // A pair without rows here meets too, as one with rows does
+                    // at its first tile: the first half's hand-over alone lets
+                    // the product write all channels, and the other half may
+                    // still be reading those of the block before.
+                    if (t == w.t0) pair_sync(pair);
+                } else if (lane == 0) {
                     mbar_arrive(&bars.p_full[m_tile][0]);
                 }
                 tc_fence_before();
@@ -1053,6 +1059,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 *swap_mine = l;
                 pair_sync(pair);
                 l = half ? *swap_other + l : l + *swap_other;
+                pair_sync(pair);  // read by both before it is written again
             }
             bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
@@ -1123,14 +1130,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 }
                 if (half == 0 && row < rows) *(float2 *)(part + S::part_ml(m_tile, row)) = make_float2(m == -INFINITY ? -INFINITY : ref, l);
             }
-            // Both of a pair have read their channels before either hands over
-            // weights of the next block, whose first product writes all
-            // channels once the first half's are there (a warp without rows
-            // there hands over at once); the exchanged sums are read as well.
-            if constexpr (S::kPaired) {
-                tc_fence_before();
-                pair_sync(pair);
-            }
+            tc_fence_before();
         }
         tc_fence_before();
     }
