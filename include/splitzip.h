@@ -618,13 +618,13 @@ sz_status sz_encode_static(const uint16_t *d_in, uint64_t n, uint8_t *d_out, uin
 sz_status sz_set_wait_limit_ns(uint64_t limit_ns);
 
 /*
- * sz_debug_set_flags -- test hook.  Bit 0: the encode, decode and
- * attention kernels' copy threads issue no bulk copy, so every stage wait of their consumer
- * threads runs out (exercises the timeout path without faulting
- * anything).  Bit 1: the decode kernel's copy thread publishes the values
- * part of its stages but never their escape part, so the consumers' wait
- * for escape records runs out after the values are stored.  0 restores
- * normal operation.
+ * sz_debug_set_flags -- test hook.  Bit 0: the encode and decode kernels'
+ * copy threads issue no bulk copy and the attention kernel's none of the
+ * cached values, so every stage wait of their consumer threads runs out
+ * (exercises the timeout path without faulting anything).  Bit 1: the
+ * decode kernel's copy thread publishes the values part of its stages but
+ * never their escape part, so the consumers' wait for escape records runs
+ * out after the values are stored.  0 restores normal operation.
  */
 sz_status sz_debug_set_flags(uint32_t flags);
 

@@ -170,6 +170,7 @@ constexpr float kRescaleAt = 8.0f;
 // Blocks up to this many tiles long are not split when there is a CTA for each
 // (one token over 333 keys, three tiles: 12.0 us, split and joined 13.4).
 constexpr uint32_t kWholeTiles = 6;
+constexpr uint64_t kLandingNs = 1000000000;              // after a failed wait, for what is still under way
 constexpr uint32_t kMaxTensorSms = 160;                 // workspace bound: CTAs = SMs * CTAs per SM
 
 template <int D, int kM>
@@ -530,8 +531,9 @@ __device__ __forceinline__ uint32_t cta_of(const PlanShared &s, uint64_t u) {
     return (uint32_t)divide((u + 1) * s.used - 1, s.total);
 }
 
-// Wait for a phase, by all lanes of a warp: false when the limit of device
-// time ran out here or elsewhere in the CTA.
+// Wait for a phase, by all lanes of a copying warp: false when the limit of
+// device time ran out here or elsewhere in the CTA (the phase may then have
+// been handed over unread, its copies still under way).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
@@ -544,7 +546,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
             }
         }
     }
-    return __all_sync(0xFFFFFFFFu, ok) != 0;
+    return __all_sync(0xFFFFFFFFu, ok && *failed == 0) != 0;
 }
 
 // The same for a role whose accesses stay in bounds whatever the data: it
@@ -666,6 +668,7 @@ struct Control {  // behind the tiles in shared memory
     Bars bars;
     PlanShared plan;
     uint32_t tmem, failed;
+    uint32_t issued[2], queries;  // uses of the ring that K's and V's copies stand behind, blocks whose queries were copied
     union {
         PlanScratch scratch;
         float swap[2][Shape<D, kM>::kPaired ? Shape<D, kM>::kRows : 1];  // between the two halves of a row: maxima, sums
@@ -754,7 +757,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         const bool one = elect_one();
         const uint32_t is_v = wid == S::kValueWarp ? 1u : 0u;
         const CUtensorMap *const map = is_v ? &v_map : &k_map;
-        const bool silent = (p.debug_flags & kDebugNoSignal) != 0;
+        const bool silent = is_v && (p.debug_flags & kDebugNoSignal) != 0;  // a test of waits that run out
         const uint32_t tile_bytes = p.key_tile * S::kHalves * kRowBytes;
         const uint32_t copy_bytes = p.box_tokens * kRowBytes;
         uint32_t use = is_v, pieces = 0;  // of the ring (K even, V odd), pieces begun
@@ -782,12 +785,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 if (one) {
                     const uint32_t rows = p.tile_tokens * p.group;
                     mbar_arrive_expect_tx(&bars.q_full[buf], tiles * rows * S::kHalves * kRowBytes);
-                    if (!silent)
-                        for (uint32_t x = 0; x < tiles; ++x)
+                    for (uint32_t x = 0; x < tiles; ++x)
 #pragma unroll
-                            for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
-                                tma_load_3d(smem0 + buf * S::kQueryBytes + x * S::kQueryTile + hf * S::kQueryHalf, &q_map, (int)(hf * 64), (int)(head * p.group),
-                                            (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full[buf]));
+                        for (uint32_t hf = 0; hf < (uint32_t)S::kHalves; ++hf)
+                            tma_load_3d(smem0 + buf * S::kQueryBytes + x * S::kQueryTile + hf * S::kQueryHalf, &q_map, (int)(hf * 64), (int)(head * p.group),
+                                        (int)((uint32_t)w.q.q0 + first + x * p.tile_tokens), smem_u32(&bars.q_full[buf]));
                 }
                 __syncwarp();
             }
@@ -825,12 +827,9 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             }
         }
         if (p.rec && is_v && lane == 0) p.rec[blockIdx.x] = rec;
-        if (!ok && !silent) {  // copies still under way must land before the CTA ends
-            // (this warp's uses of the last round of slots)
-            for (uint32_t u = use > 2 * S::kSlots ? use - 2 * S::kSlots : is_v; u < use; u += 2)
-                mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, limit);
-            for (uint32_t u = pieces > S::kQueries ? pieces - S::kQueries : 0; u < pieces; ++u)
-                mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, limit);
+        if (lane == 0) {
+            control.issued[is_v] = use;
+            if (!is_v) control.queries = pieces;
         }
         } else if (wid >= kMmaWarp && wid < kMmaWarp + S::kMmaWarps) {
         // ---------------------------------------------------------- products
@@ -923,13 +922,6 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 if (more && one) mma_commit(&bars.empty[slot]);
                 if (more) pass();
             }
-        }
-        if (*fail) {  // products under way must end before their memory is given back
-            if (one) {
-                mma_commit(&bars.drain[mine]);
-                mbar_wait(&bars.drain[mine], 0, limit);
-            }
-            __syncwarp();
         }
         }
     } else {
@@ -1153,6 +1145,28 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     // ------------------------------------------------------------------ end
     __syncthreads();
     if (failed) {  // rows may be unfinished: no result of this call stands
+        // Products and copies under way must end before the memory that they
+        // write is given back.  They get a second, however short the limit.
+        const uint64_t patience = umax64(limit, kLandingNs);
+        if (wid >= kMmaWarp && wid < kMmaWarp + S::kMmaWarps) {
+            uint64_t *const drain = &bars.drain[wid - kMmaWarp];
+            if (elect_one()) {
+                mma_commit(drain);
+                mbar_wait(drain, 0, patience);
+            }
+            __syncwarp();
+        }
+        if (wid == S::kKeyWarp) {
+            const uint32_t kinds = (p.debug_flags & kDebugNoSignal) != 0 ? 1 : 2;
+            for (uint32_t kind = 0; kind < kinds; ++kind) {  // the last use of each slot is among these
+                const uint32_t end = control.issued[kind];
+                for (uint32_t u = end > 2 * S::kSlots ? end - 2 * S::kSlots : kind; u < end; u += 2)
+                    mbar_wait(&bars.full[u % S::kSlots], u / S::kSlots & 1, patience);
+            }
+            const uint32_t end = control.queries;
+            for (uint32_t u = end > S::kQueries ? end - S::kQueries : 0; u < end; ++u)
+                mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, patience);
+        }
         if (tid == 0) {
             atomicExch(p.timed_out, p.call);
             __threadfence();

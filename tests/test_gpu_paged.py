@@ -263,6 +263,31 @@ def test_waits_that_run_out_are_reported():
         assert not status.any() and torch.equal(again, good)
 
 
+@pytest.mark.parametrize("new,kv,dim", [([1, 2] * 30, [3000, 70] * 30, 128), ([5] * 12, [900] * 12, 64), ([300, 200], [900, 2000], 64),
+                                        ([700, 90], [1500, 1203], 128)], ids=["few128", "few64", "many64", "many128"])
+@pytest.mark.parametrize("limit", [0, 1, 1000, 5000])
+def test_waits_that_run_out_with_copies_under_way(new, kv, dim, limit):
+    # limits shorter than a copy takes (a wait that the hardware ends before it
+    # looks at the clock is none that ran out): the call ends with one status for
+    # all, after everything that it set going, and the next one is as good as ever
+    b = Batch(new, kv, 8, 2, dim, 16, BF16)
+    args = [b.q.to(DEV)] + b.cache()
+    ws = torch.empty(sz.sz_plan_attention(dim), dtype=torch.uint8, device=DEV)
+    good = sz.paged_attention(*args, workspace=ws)[0].clone()
+    for _ in range(4):
+        try:
+            sz.sz_set_wait_limit_ns(limit)
+            out, _, status = sz.paged_attention(*args, workspace=ws)
+            torch.cuda.synchronize()
+        finally:
+            sz.sz_set_wait_limit_ns(1_000_000_000)
+        got = set(status.cpu().tolist())
+        assert got in ({0}, {sz.SZ_ERR_DEVICE_TIMEOUT})
+        assert got != {0} or torch.equal(out, good)
+        again, _, status = sz.paged_attention(*args, workspace=ws)
+        assert not status.any() and torch.equal(again, good)
+
+
 @pytest.mark.parametrize("new,kv,dim", [([5] * 12, [40] * 12, 128), ([7], [200], 64), ([200], [200], 128), ([4, 3], [5000, 70], 128)], ids=str)
 def test_hidden_values_with_the_output_over_the_queries(new, kv, dim):
     # such rows are computed from their queries once more, which stay until
