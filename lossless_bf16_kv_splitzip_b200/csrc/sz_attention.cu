@@ -531,36 +531,38 @@ __device__ __forceinline__ uint32_t cta_of(const PlanShared &s, uint64_t u) {
     return (uint32_t)divide((u + 1) * s.used - 1, s.total);
 }
 
-// Wait for a phase, by all lanes of a copying warp: false when the limit of
-// device time ran out here or elsewhere in the CTA (the phase may then have
-// been handed over unread, its copies still under way).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!(ok = mbar_try_wait(bar, parity))) {
-            if (*failed) break;
-            if (globaltimer_ns() - t0 > limit_ns) {
-                *failed = 1u;
-                break;
-            }
-        }
-    }
-    return __all_sync(0xFFFFFFFFu, ok && *failed == 0) != 0;
-}
+// What the roles of a CTA tell one another beside its barriers: that a wait
+// ran out, and how many warps sum rows again (mend_rows), which may take longer
+// than any wait should.
+struct Watch {
+    uint32_t failed, busy;
+};
 
-// The same for a role whose accesses stay in bounds whatever the data: it
-// goes on after a failure, which ends all further waits at once.
-__device__ __forceinline__ void wait_or_fail(uint64_t *bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = globaltimer_ns();
+// Wait for a phase; false when the limit of device time ran out here or
+// elsewhere in the CTA.
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile Watch *watch, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
-        if (*failed) break;
+        if (watch->failed) return false;
         if (globaltimer_ns() - t0 > limit_ns) {
-            *failed = 1u;
-            break;
+            if (watch->busy) {
+                t0 = globaltimer_ns();
+                continue;
+            }
+            watch->failed = 1u;
+            return false;
         }
     }
+    return true;
+}
+// The roles whose accesses stay in bounds whatever the data go on after a
+// failure, which ends all further waits at once.  A copying warp asks this,
+// for all of its lanes, and stops: a phase may have been handed over unread,
+// its copies still under way.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile Watch *watch, uint64_t limit_ns) {
+    const bool ok = wait_or_fail(bar, parity, watch, limit_ns);
+    return __all_sync(0xFFFFFFFFu, ok && watch->failed == 0) != 0;
 }
 
 // Columns outside [from, to) of a row's scores become -inf.
@@ -592,68 +594,179 @@ __device__ __forceinline__ bool asks(uint32_t pair, bool x) {
     return __any_sync(0xFFFFFFFFu, x) != 0;
 }
 
-// One row's accumulator over the visible ones of keys [from, to), by one
-// warp: sum 2^(c s_j - ref) v_j.  A key hidden from a row has weight 0 in the
-// products, and 0 * inf there is NaN: a row whose accumulator holds a NaN
-// while its sum does not is computed again here from the keys it sees alone.
-// (If one of those is the reason, the loop ends when every channel is NaN.)
-// Writes channels 8 * own_begin .. (8 * own of them) of the scaled 16-bit row
-// to `out`, or of the 32-bit one to `part`; where `out` lies over the queries
-// and two warps share the row, `pair` is their barrier, and neither writes
-// before both have read.
-template <typename T, int D>
-__device__ __noinline__ void visible_row(const TensorArgs *p, uint32_t r, uint32_t kv_head, const uint16_t *q, int32_t from, int32_t to,
-                                         float ref, float inv, uint16_t *out, float *part, uint32_t part_step, uint32_t own_begin, uint32_t own,
-                                         uint32_t pair) {
-    constexpr uint32_t kLanes = D / 8, kGroups = 32 / kLanes;  // lanes per key, keys at a time
+// Which of two 16-bit values are infinite or NaN: bits 0 and 16.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+    constexpr uint32_t kExponent = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+    return ((pair & kExponent) == kExponent ? 1u : 0u) | ((pair >> 16 & kExponent) == kExponent ? 0x10000u : 0u);
+}
+
+// Rows (one per lane, where `odd`) whose accumulator holds a NaN while their
+// sum does not: somewhere a weight met a value that is not finite.  It was the
+// weight of a key that the row sees, whose infinity or NaN belongs in the
+// result (also where the weight was so small that it became 0 in 16 bits, and
+// 0 times infinity NaN), or the 0 of a hidden key, whose value does not.  So
+// the keys that the row sees, [from, to) of those in hand, are looked through
+// for such values, a key per lane at a time, and what they come to replaces
+// the accumulator's NaNs: an infinity where only values of its sign were met,
+// NaN where both were, or a NaN, or a key of weight exactly 0.  A NaN that met
+// none came from a hidden key: that channel is summed again, 2^(c s_j - ref) v_j
+// over the keys that the row sees.  `o_at` holds channels [c0, c0 + kOwn).
+// Both are bound by the latency of a key's loads.  A chunk of 4,096 tokens over
+// 32,768 keys (32 heads of 128, 1.65 ms) takes no longer where all rows see an
+// infinity, 115 ms where a channel is infinite in every key, 160 ms where the
+// last token's value is NaN and the two blocks per KV head that must not see it
+// are summed again.
+template <typename T, int D, int kOwn>
+__device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32_t r, uint32_t kv_head, const uint16_t *q, bool odd, int32_t from,
+                                       int32_t to, float ref, uint32_t o_at, uint32_t c0) {
+    constexpr int kWords = kOwn / 32;  // a bit per channel
     const sz_paged_kv &kv = p->kv;
-    const uint32_t lane = threadIdx.x & 31, l = lane % kLanes, group = lane / kLanes;
-    float x[8], o[8] = {};
-    widen8<T>(*(const uint4 *)(q + l * 8), x);
-    for (int32_t j0 = from; j0 < to; j0 += (int32_t)kGroups) {
-        const int32_t j = j0 + (int32_t)group;
-        const int32_t page = j < to ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
-        const uint32_t slot = (uint32_t)j % kv.page_tokens;
-        float k[8] = {}, v[8] = {};
-        if (page >= 0) {
-            widen8<T>(*(const uint4 *)((const uint16_t *)kv.d_k + (uint64_t)page * kv.k_stride[0] + kv_head * kv.k_stride[1] +
-                                       slot * kv.k_stride[2] + l * 8), k);
-            widen8<T>(*(const uint4 *)((const uint16_t *)kv.d_v + (uint64_t)page * kv.v_stride[0] + kv_head * kv.v_stride[1] +
-                                       slot * kv.v_stride[2] + l * 8), v);
-        }
+    const uint32_t lane = threadIdx.x & 31;
+    if (lane == 0) atomicAdd(&watch->busy, 1u);
+    uint32_t nan[kWords], up[kWords] = {}, down[kWords] = {};
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        uint32_t o[32];
+        tmem_ld32(o_at + w * 32, o);
+        tmem_wait_ld();
+        nan[w] = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (odd && __uint_as_float(o[i]) != __uint_as_float(o[i])) nan[w] |= 1u << i;
+    }
+    const uint16_t *const keys = (const uint16_t *)kv.d_k + kv_head * kv.k_stride[1];
+    const uint16_t *const values = (const uint16_t *)kv.d_v + kv_head * kv.v_stride[1] + c0;
+    auto score = [&](const uint16_t *k) {
         float s = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < D; i += 8) {
+            float a[8], b[8];
+            widen8<T>(*(const uint4 *)(q + i), a);
+            widen8<T>(*(const uint4 *)(k + i), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[i] * k[i];
-#pragma unroll
-        for (int d = kLanes / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        bool gone = true;
-        if (page >= 0) {
-            const float w = exp2f(fmaf(s, p->c, -ref));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] += w * v[i];
+            for (int e = 0; e < 8; ++e) s += a[e] * b[e];
         }
+        return s;
+    };
+    bool q_infinite = false;
+    if (odd)
+        for (int i = 0; i < D; i += 2) q_infinite |= not_finite<T>(*(const uint32_t *)(q + i)) != 0;
+    const int32_t first = __reduce_min_sync(0xFFFFFFFFu, odd ? from : 0x7FFFFFFF), end = __reduce_max_sync(0xFFFFFFFFu, odd ? to : 0);
+    bool open = true;  // some row's NaN is not explained for good
+    for (int32_t j0 = first; open && j0 < end; j0 += 32) {
+        const int32_t j = j0 + (int32_t)lane;
+        const int32_t page = j < end ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
+        const uint32_t slot = (uint32_t)j % kv.page_tokens;
+        uint32_t found = 0;
+        if (page >= 0) {
+            const uint16_t *const v = values + (uint64_t)page * kv.v_stride[0] + slot * kv.v_stride[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gone &= o[i] != o[i];
-        const uint32_t all = __ballot_sync(0xFFFFFFFFu, gone);
-        bool end = false;
+            for (int i = 0; i < kOwn / 8; ++i) {
+                const uint4 y = *(const uint4 *)(v + i * 8);
+                found |= not_finite<T>(y.x) | not_finite<T>(y.y) | not_finite<T>(y.z) | not_finite<T>(y.w);
+            }
+        }
+        uint32_t hits = __ballot_sync(0xFFFFFFFFu, found != 0);
+        while (open && hits) {
+            const int src = __ffs(hits) - 1;
+            hits &= hits - 1;
+            const int32_t key = j0 + src;
+            const uint64_t key_page = (uint64_t)__shfl_sync(0xFFFFFFFFu, page, src), key_slot = __shfl_sync(0xFFFFFFFFu, slot, src);
+            const uint16_t *const v = values + key_page * kv.v_stride[0] + key_slot * kv.v_stride[2];
+            const bool sees = odd && key >= from && key < to;
+            // weight 0: a score of -inf, which finite numbers come to by
+            // overflow at most
+            const uint16_t *const k = keys + key_page * kv.k_stride[0] + key_slot * kv.k_stride[2];
+            bool infinite = q_infinite;
+            for (uint32_t i = 2 * lane; i < D; i += 64) infinite |= not_finite<T>(*(const uint32_t *)(k + i)) != 0;
+            const bool nothing = __any_sync(0xFFFFFFFFu, infinite) && sees && score(k) == -INFINITY;
+            bool more = false;
 #pragma unroll
-        for (uint32_t g = 0; g < kGroups; ++g) end |= (all >> (g * kLanes) & ((1ull << kLanes) - 1)) == (1ull << kLanes) - 1;
-        if (end) break;
+            for (int w = 0; w < kWords; ++w) {
+                const uint32_t bits = v[w * 32 + lane];
+                const float y = Half2<T>::widen(bits).x;
+                const bool any = not_finite<T>(bits) != 0;
+                const uint32_t up1 = __ballot_sync(0xFFFFFFFFu, any && !(y < 0.0f)), down1 = __ballot_sync(0xFFFFFFFFu, any && !(y > 0.0f));
+                if (sees) {
+                    up[w] |= nothing ? up1 | down1 : up1;
+                    down[w] |= nothing ? up1 | down1 : down1;
+                }
+                more |= (nan[w] & ~(up[w] & down[w])) != 0;
+            }
+            open = __any_sync(0xFFFFFFFFu, more) != 0;
+        }
     }
 #pragma unroll
-    for (uint32_t d = kLanes; d < 32; d <<= 1)
+    for (int w = 0; w < kWords; ++w) {
+        const uint32_t lost = nan[w] & ~(up[w] | down[w]);
+        float o[32] = {};
+        const int32_t end1 = __reduce_max_sync(0xFFFFFFFFu, lost ? to : 0);
+#pragma unroll 1
+        for (int32_t j0 = __reduce_min_sync(0xFFFFFFFFu, lost ? from : 0x7FFFFFFF); j0 < end1; j0 += 32) {
+            const int32_t j = j0 + (int32_t)lane;
+            const int32_t page = j < end1 ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
+            const uint32_t here = __ballot_sync(0xFFFFFFFFu, page >= 0);
+            // keys without a page: the pool's first, with weight 0
+            const uint64_t page1 = page >= 0 ? (uint32_t)page : 0, slot = page >= 0 ? (uint32_t)j % kv.page_tokens : 0;
+            const uint64_t k_at = (uint64_t)(keys + page1 * kv.k_stride[0] + slot * kv.k_stride[2]);
+            const uint64_t v_at = (uint64_t)(values + page1 * kv.v_stride[0] + slot * kv.v_stride[2] + w * 32);
+#pragma unroll 1
+            for (int t = 0; t < 32; t += 2) {
+                // two keys at a time, which share the loads of q; those after next are on their way to the first cache
+                const int ahead = (t + 4 + (int)(lane / 16)) & 31;
+                const uint64_t k_ahead = __shfl_sync(0xFFFFFFFFu, k_at, ahead), v_ahead = __shfl_sync(0xFFFFFFFFu, v_at, ahead);
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(k_ahead + lane % 16 * (D / 8)));
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(v_ahead + lane % 16 * 4));
+                const uint16_t *const k0 = (const uint16_t *)__shfl_sync(0xFFFFFFFFu, k_at, t), *const k1 = (const uint16_t *)__shfl_sync(0xFFFFFFFFu, k_at, t + 1);
+                const uint16_t *const v0 = (const uint16_t *)__shfl_sync(0xFFFFFFFFu, v_at, t), *const v1 = (const uint16_t *)__shfl_sync(0xFFFFFFFFu, v_at, t + 1);
+                const bool sees0 = lost && j0 + t >= from && j0 + t < to && (here >> t & 1u), sees1 = lost && j0 + t + 1 >= from && j0 + t + 1 < to && (here >> t & 2u);
+                if (!sees0 && !sees1) continue;
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 8) {
+                    float a[8], b[8];
+                    widen8<T>(*(const uint4 *)(q + i), a);
+                    widen8<T>(*(const uint4 *)(k0 + i), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xFFFFFFFFu, o[i], d);
-    if (pair) pair_sync(pair);
-    if (group != 0 || l < own_begin || l >= own_begin + own) return;
-    if (out) {
+                    for (int e = 0; e < 8; ++e) s0 += a[e] * b[e];
+                    widen8<T>(*(const uint4 *)(k1 + i), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= inv;
-        *(uint4 *)(out + l * 8) = narrow8<T>(o);
-    } else {
-        *(float4 *)(part + (2 * l) * part_step) = make_float4(o[0], o[1], o[2], o[3]);
-        *(float4 *)(part + (2 * l + 1) * part_step) = make_float4(o[4], o[5], o[6], o[7]);
+                    for (int e = 0; e < 8; ++e) s1 += a[e] * b[e];
+                }
+                const float e0 = exp2f(fmaf(s0, p->c, -ref)), e1 = exp2f(fmaf(s1, p->c, -ref));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y[8];
+                    widen8<T>(*(const uint4 *)(v0 + i * 8), y);
+                    if (sees0)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) o[i * 8 + c] += e0 * y[c];
+                    widen8<T>(*(const uint4 *)(v1 + i * 8), y);
+                    if (sees1)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) o[i * 8 + c] += e1 * y[c];
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t a[16];
+            tmem_ld16(o_at + w * 32 + h * 16, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t bit = 1u << (h * 16 + i);
+                if (lost & bit) a[i] = __float_as_uint(o[h * 16 + i]);
+                if (nan[w] & (up[w] ^ down[w]) & bit) a[i] = up[w] & bit ? 0x7F800000u : 0xFF800000u;
+            }
+            tmem_st16(o_at + w * 32 + h * 16, a);
+        }
     }
+    tmem_wait_st();
+    if (lane == 0) atomicSub(&watch->busy, 1u);
+    __syncwarp();
 }
 
 struct Bars {
@@ -667,7 +780,8 @@ template <int D, int kM>
 struct Control {  // behind the tiles in shared memory
     Bars bars;
     PlanShared plan;
-    uint32_t tmem, failed;
+    uint32_t tmem;
+    Watch watch;
     uint32_t issued[2], queries;  // uses of the ring that K's and V's copies stand behind, blocks whose queries were copied
     union {
         PlanScratch scratch;
@@ -689,7 +803,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     Control &control = *reinterpret_cast<Control *>(raw + S::kData);
     Bars &bars = control.bars;
     PlanShared &plan = control.plan;
-    uint32_t &failed = control.failed;
+    const volatile uint32_t &failed = control.watch.failed;
     // what is the same for a whole warp is passed through a shuffle, so that
     // the compiler keeps it in uniform registers, where the tensor
     // instructions want their operands
@@ -718,7 +832,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
         mbar_init(&bars.drain[0], 1);
         mbar_init(&bars.drain[1], 1);
         fence_mbar_init();
-        failed = 0;
+        control.watch.failed = control.watch.busy = 0;
     }
     if (wid == S::kKeyWarp && lane == 0) {
         prefetch_map(&q_map);
@@ -747,7 +861,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
     cur.left = plan.left;
     cur.whole = plan.whole;
     cur.q = plan.q;
-    volatile uint32_t *const fail = &failed;
+    volatile Watch *const watch = &control.watch;
     const uint64_t limit = p.wait_limit_ns;
     Piece w;
     if (!softmax) {
@@ -780,7 +894,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             const uint32_t head = same(w.head);
             if (!is_v) {
                 const uint32_t buf = pieces % S::kQueries;
-                if (!(ok = warp_wait(&bars.q_empty[buf], (pieces / S::kQueries & 1) ^ 1, fail, limit))) break;
+                if (!(ok = warp_wait(&bars.q_empty[buf], (pieces / S::kQueries & 1) ^ 1, watch, limit))) break;
                 ++pieces;
                 if (one) {
                     const uint32_t rows = p.tile_tokens * p.group;
@@ -810,7 +924,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             for (int32_t t = (int32_t)same((uint32_t)w.t0); t < t_end; ++t, use += 2) {
                 const int32_t token = p.box_tokens < p.kv.page_tokens ? t * (int32_t)p.key_tile % (int32_t)p.kv.page_tokens : 0;
                 const uint32_t slot = use % S::kSlots, phase = use / S::kSlots & 1;
-                if (!(ok = warp_wait(&bars.empty[slot], phase ^ 1, fail, limit))) break;
+                if (!(ok = warp_wait(&bars.empty[slot], phase ^ 1, watch, limit))) break;
                 const uint32_t bar = smem_u32(&bars.full[slot]);
                 if (one) mbar_arrive_expect_tx(&bars.full[slot], tile_bytes);
                 uint32_t dst = ring0 + slot * S::kTileBytes;
@@ -849,7 +963,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 for (uint32_t m = 0; m < kM; ++m) f(m);
             }
         };
-        for (uint32_t piece = 0; same(*fail) == 0; ++piece) {
+        for (uint32_t piece = 0; same(failed) == 0; ++piece) {
             if (same(next_piece<D, kM>(p, cur, w) ? 1u : 0u) == 0) break;
             const int32_t t_begin = (int32_t)same((uint32_t)w.t0), t_end = (int32_t)same((uint32_t)w.t1), kv = (int32_t)same((uint32_t)w.q.kv);
             const uint32_t tiles = same(kM == 1 || (uint32_t)w.q.n - w.block * kM * p.tile_tokens <= p.tile_tokens ? 1u : 2u);  // row tiles in use
@@ -866,8 +980,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 }
                 __syncwarp();
             };
-            wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, fail, limit);
-            wait_or_fail(&bars.full[slot], phase, fail, limit);
+            wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, watch, limit);
+            wait_or_fail(&bars.full[slot], phase, watch, limit);
             tc_fence_after();
             each([&](uint32_t m) {
                 if (m < tiles) score(m);
@@ -877,10 +991,10 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             for (int32_t t = t_begin; t < t_end; ++t) {
                 const uint32_t v_slot = slot;
                 const bool more = t + 1 < t_end;
-                wait_or_fail(&bars.full[slot], phase, fail, limit);
+                wait_or_fail(&bars.full[slot], phase, watch, limit);
                 pass();
                 if (more)  // the next K now, so that nothing is waited for between the products
-                    wait_or_fail(&bars.full[slot], phase, fail, limit);
+                    wait_or_fail(&bars.full[slot], phase, watch, limit);
                 else if (one)
                     mma_commit(&bars.q_empty[buf]);
                 // keys behind the last token in this tile's last page: their
@@ -903,7 +1017,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                     if (m < tiles) {
 #pragma unroll
                         for (uint32_t part = 0; part < 2; ++part) {  // the weights of 64 keys each
-                            wait_or_fail(&bars.p_full[m][part], (S::kMmaWarps == 1 && m == 1 ? done2 : done) & 1, fail, limit);
+                            wait_or_fail(&bars.p_full[m][part], (S::kMmaWarps == 1 && m == 1 ? done2 : done) & 1, watch, limit);
                             tc_fence_after();
                             if (one) {
 #pragma unroll
@@ -949,7 +1063,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             float m = -INFINITY;             // reference of the weights
             uint64_t sum = pack2(0.0f, 0.0f);  // of this half's weights, in two parts
             for (int32_t t = w.t0; t < w.t1; ++t, ++n) {
-                wait_or_fail(&bars.s_full[m_tile], n & 1, fail, limit);
+                wait_or_fail(&bars.s_full[m_tile], n & 1, watch, limit);
                 tc_fence_after();
                 if (warp_live) {
                     // this row's visible columns; all of them in most tiles
@@ -985,7 +1099,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             m = high;
                         } else {
                             // the accumulator as of the tile before
-                            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
+                            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, watch, limit);
                             tc_fence_after();
                             const bool rise = (high - m) * p.c > kRescaleAt;
                             const float f = rise ? exp2_fast((m - high) * p.c) : 1.0f;
@@ -1042,7 +1156,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.p_full[m_tile][kParts == 2 ? 1 : half]);
             }
-            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, fail, limit);
+            wait_or_fail(&bars.pv_done[m_tile], (n - 1) & 1, watch, limit);
             tc_fence_after();
             if (!warp_live) continue;
             const float2 both = unpack2(sum);
@@ -1053,7 +1167,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 l = half ? *swap_other + l : l + *swap_other;
                 pair_sync(pair);  // read by both before it is written again
             }
-            bool mine = row < rows;
+            const bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
             const float ref = m * p.c;  // log2 units
             const bool whole = w.starts && w.ends, any = begin < stop;
@@ -1071,28 +1185,14 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 for (int j = 0; j < 16; ++j) seen = add2(seen, pack2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])));
             }
             const float2 seen2 = unpack2(seen);
-            uint32_t odd = __ballot_sync(0xFFFFFFFFu, mine && seen2.x + seen2.y != seen2.x + seen2.y && l > 0.0f && *fail == 0);
-            const bool shared_rows = S::kPaired && whole && (const void *)p.a.d_out == p.a.d_q;
-            if constexpr (S::kPaired)
-                if (shared_rows && pair_any(pair, odd != 0)) {  // then both take the same rows
-                    *swap_mine = __uint_as_float(odd);
-                    pair_sync(pair);
-                    odd |= __float_as_uint(*swap_other);
-                    pair_sync(pair);
-                }
-            if (odd >> lane & 1u) mine = false;
-            while (odd) {
-                const int src = __ffs(odd) - 1;
-                odd &= odd - 1;
-                const uint32_t t = __shfl_sync(0xFFFFFFFFu, token, src), h = __shfl_sync(0xFFFFFFFFu, head, src);
-                const int32_t from = max(__shfl_sync(0xFFFFFFFFu, begin, src), w.t0 * (int32_t)p.key_tile);
-                const int32_t to = min(__shfl_sync(0xFFFFFFFFu, stop, src), w.t1 * (int32_t)p.key_tile);
-                const float ref1 = __shfl_sync(0xFFFFFFFFu, ref, src), inv1 = __shfl_sync(0xFFFFFFFFu, inv, src);
-                uint16_t *const out1 = whole ? (uint16_t *)p.a.d_out + (uint64_t)t * p.a.out_stride[0] + (uint64_t)h * p.a.out_stride[1] : nullptr;
-                visible_row<T, D>(&p, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)t * p.a.q_stride[0] + (uint64_t)h * p.a.q_stride[1], from, to,
-                                  ref1, inv1, out1, part + S::part_o(m_tile, 0, lanes + src), S::part_o(0, 1, 0), half * (kOwn / 8), kOwn / 8,
-                                  shared_rows ? pair : 0u);
-            }
+            const bool odd = mine && seen2.x + seen2.y != seen2.x + seen2.y && l > 0.0f && failed == 0;
+            // where the output lies over the queries, neither of a pair may
+            // write before both have read
+            const bool wait_both = S::kPaired && whole && (const void *)p.a.d_out == p.a.d_q && pair_any(pair, odd);
+            if (__any_sync(0xFFFFFFFFu, odd))
+                mend_rows<T, D, (int)kOwn>(&p, &control.watch, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)token * p.a.q_stride[0] + (uint64_t)head * p.a.q_stride[1],
+                                           odd, max(begin, w.t0 * (int32_t)p.key_tile), min(stop, w.t1 * (int32_t)p.key_tile), ref, o_at, half * kOwn);
+            if (wait_both) pair_sync(pair);
             if (whole) {
 #pragma unroll
                 for (int i = 0; i < (int)kOwn / 32; ++i) {

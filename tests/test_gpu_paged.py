@@ -217,6 +217,96 @@ def test_values_hidden_from_a_row_do_not_reach_it(shape, value):
         check(out[new[0] - 1, :, same], want[0][new[0] - 1, :, same], want[2][new[0] - 1, :, same]) if not window else None
 
 
+def spoil(b, values, hidden=None):
+    """Values of request 0, (key, channel, value), put into b.v; what a row
+    that sees them comes to: a list of (key, channel, value) for expect()."""
+    for key, channel, value in values + ([hidden] if hidden else []):
+        b.v[int(b.table[0, key // b.page]), :, key % b.page, channel] = value
+
+
+def expect(want, tol, p, values, window=0):
+    """The definition's result where values (key, channel, value) of request 0
+    are not finite: rows at positions p that see them hold +-inf, or NaN where
+    both signs or a NaN meet."""
+    want, tol = want.clone(), tol.clone()
+    for channel in {c for _, c, _ in values}:
+        met = torch.zeros(len(p), dtype=torch.float64)
+        for key, c, value in values:
+            if c == channel:
+                met[(p >= key) & ((p - window < key) if window else True)] += value
+        rows = met != 0  # inf, -inf or NaN
+        want[: len(p), :, channel][rows] = met[rows, None]
+        tol[: len(p), :, channel][rows] = 0.0
+    return want, tol
+
+
+def check_with_nan(got, want, tol, what=""):
+    got = got.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan()), what + ": NaN in other places"
+    check(torch.nan_to_num(got, nan=0.0, posinf=math.inf, neginf=-math.inf), torch.nan_to_num(want, nan=0.0, posinf=math.inf, neginf=-math.inf), tol, what)
+
+
+INF = math.inf
+SPOILED = {  # values that rows see, (key, channel, value), and one that the last row alone sees
+    "early": ([(5, 3, INF)], None),
+    "early_nan": ([(5, 3, math.nan)], None),
+    "both_signs": ([(5, 3, INF), (70, 3, -INF), (70, 60, -INF)], None),
+    "early_and_last": ([(5, 3, -INF)], (None, 40, INF)),
+    "last": ([], (None, 9, math.nan)),
+    "a_channel": ([(key, 17, INF) for key in range(2000)], None),
+}
+
+
+@pytest.mark.parametrize("case", SPOILED)
+@pytest.mark.parametrize("new,kv,hq,hk,dim,dtype", [([300, 5], [20000, 40], 2, 1, 128, BF16), ([300], [20000], 2, 2, 64, FP16), ([6, 1], [20000, 300], 8, 1, 128, FP16),
+                                                    ([7], [9000], 4, 2, 64, BF16)], ids=["chunk128", "chunk64", "few128", "few64"])
+def test_values_that_are_not_finite_in_long_caches(case, new, kv, hq, hk, dim, dtype):
+    # a row that sees one has it in its result, whatever the weight; a row that
+    # does not is computed from what it sees; neither costs the call its status,
+    # though computing rows again may take longer than a wait is allowed to
+    b = Batch(new, kv, hq, hk, dim, 16, dtype, seed=41)
+    values, hidden = SPOILED[case]
+    hidden = hidden and (kv[0] - 1, hidden[1], hidden[2])
+    want, wl, tol, tl = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    spoil(b, values, hidden)
+    p = torch.arange(kv[0] - new[0], kv[0])
+    want, tol = expect(want, tol, p, values + ([hidden] if hidden else []))
+    k, v, table, q_begin, kv_len = b.cache()
+    try:
+        sz.sz_set_wait_limit_ns(20_000_000)
+        out, lse, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, return_lse=True)
+        torch.cuda.synchronize()
+    finally:
+        sz.sz_set_wait_limit_ns(1_000_000_000)
+    assert not status.any()
+    check_with_nan(out, want, tol, "out")
+    check(lse, wl, tl, "lse")
+
+
+@pytest.mark.parametrize("new,hq", [(200, 1), (3, 4)])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("over", [False, True])
+def test_infinities_of_small_weights(new, hq, dtype, over):
+    # keys whose weights are far below what 16 bits hold: an infinite value of
+    # theirs is in the result all the same, and NaN where the score is -inf
+    dim, kv = 128, 260
+    b = Batch([new], [kv], hq, 1, dim, 16, dtype, seed=42)
+    b.q = b.q.abs() + 0.5
+    for key in (2, 7):  # scores about 10 below the others': exp(-30) or so
+        b.k[int(b.table[0, 0]), 0, key] = -4.0
+    want, _, tol, _ = ref.attention(b.q, b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    spoil(b, [(2, 3, INF), (7, 50, -INF), (7, 3, INF)])
+    want, tol = expect(want, tol, torch.arange(kv - new, kv), [(2, 3, INF), (7, 50, -INF)])
+    k, v, table, q_begin, kv_len = b.cache()
+    q = b.q.to(DEV)
+    out, _, status = sz.paged_attention(q, k, v, table, q_begin, kv_len, out=q if over else None)
+    assert not status.any()
+    check_with_nan(out, want, tol)
+    k[int(b.table[0, 0]), 0, 7] = -math.inf  # weight 0 exactly
+    out, _, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len)
+    assert not status.any() and bool(out[:, :, 50].isnan().all()) and bool(out[:, :, 3].isnan().all())
+
+
 @pytest.mark.parametrize("dim,hidden", [(128, None), (128, math.inf), (64, None), (64, math.nan)], ids=str)
 def test_short_blocks_behind_long_ones(dim, hidden):
     # a CTA's blocks of 64 and of 8 rows in turn: a warp that holds rows of the
