@@ -167,6 +167,14 @@ constexpr uint32_t kTileRows = 128;
 constexpr uint32_t kRowBytes = 128;                    // 64 values: one swizzled row
 constexpr uint32_t kHalfBytes = kTileRows * kRowBytes;  // 64 channels of a tile
 constexpr float kRescaleAt = 8.0f;
+// Weights are handed to the products in 16 bits.  FP16 holds none below 2^-25,
+// so they are taken 2^7 times larger there, up to 2^15 in all: a key is lost
+// below 2^-32 of the largest, and 131,072 lost ones weigh less than a
+// sixteenth of half a step.  BF16 has the range of 32 bits.
+template <typename T>
+__device__ __forceinline__ float reference(float m, float c) {
+    return fmaf(m, c, std::is_same<T, __half>::value ? -7.0f : 0.0f);
+}
 // Blocks up to this many tiles long are not split when there is a CTA for each
 // (one token over 333 keys, three tiles: 12.0 us, split and joined 13.4).
 constexpr uint32_t kWholeTiles = 6;
@@ -1119,9 +1127,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             if constexpr (S::kPaired) pair_sync(pair);  // the other's channels too, before any weight is handed over
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.0f : m * p.c;
+                    const float ref = m == -INFINITY ? 0.0f : reference<T>(m, p.c);
                     const uint64_t c2 = pack2(p.c, p.c), ref2 = pack2(-ref, -ref);
-                    uint64_t sum1 = pack2(0.0f, 0.0f);
+                    // summed by tile first: a small weight beside a large running
+                    // sum would be lost, 128 of them less so
+                    uint64_t sum0 = pack2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
                     for (uint32_t i = 0; i < kParts * 2; ++i) {  // weights of 64 columns take the first 32 of them
                         uint32_t w16[16];
@@ -1130,7 +1140,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             const int at = (int)(i & 1) * 32 + 2 * j;
                             const uint64_t x = fma2(pack2(__uint_as_float(s[i / 2][at]), __uint_as_float(s[i / 2][at + 1])), c2, ref2);
                             const float2 y = unpack2(x), e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                            if (j & 1) sum1 = add2(sum1, pack2(e.x, e.y)); else sum = add2(sum, pack2(e.x, e.y));
+                            if (j & 1) sum1 = add2(sum1, pack2(e.x, e.y)); else sum0 = add2(sum0, pack2(e.x, e.y));
                             w16[j] = Half2<T>::narrow(e.x, e.y);
                         }
                         tmem_st16(s_at + (i / 2) * 64 + (i & 1) * 16, w16);
@@ -1141,7 +1151,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             if (lane == 0) mbar_arrive(&bars.p_full[m_tile][0]);
                         }
                     }
-                    sum = add2(sum, sum1);
+                    sum = add2(sum, add2(sum0, sum1));
                     tmem_wait_st();
                 } else if (S::kPaired) {
                     // A pair without rows here meets too, as one with rows does
@@ -1169,7 +1179,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             }
             const bool mine = row < rows;
             const uint32_t token = (uint32_t)w.q.q0 + first + my_token, head = w.head * p.group + my_head;
-            const float ref = m * p.c;  // log2 units
+            const float ref = reference<T>(m, p.c);  // log2 units
             const bool whole = w.starts && w.ends, any = begin < stop;
             const float inv = any ? 1.0f / l : 0.0f;
             uint16_t *const out = (uint16_t *)p.a.d_out + (uint64_t)token * p.a.out_stride[0] + (uint64_t)head * p.a.out_stride[1];

@@ -395,6 +395,36 @@ def test_hidden_values_with_the_output_over_the_queries(new, kv, dim):
         assert torch.equal(over.view(torch.int16), apart.view(torch.int16))
 
 
+@pytest.mark.parametrize("dtype", [FP16, BF16])
+@pytest.mark.parametrize("reqs,new", [(1, 4864), (40, 1)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_small_weights_behind_one_large(dtype, reqs, new, dim):
+    # one key with value 0, 131,071 with value 1 whose weights are 2^-25.5 of its:
+    # together 2^-8.5.  A weight is off by half a step of 16 bits, or half of FP16's
+    # smallest step, 2^-25 against a sum of at least 2^7: n 2^-32 in all.  The sums
+    # of weights take 32 steps in a tile and n / 128 tiles, each off by 2^-24: 2^-13.9
+    # together; those of weights times values n / 16 steps, cut off at 2^-23: 2^-10.
+    # The exponential's argument of 25.5 adds 2^-18, and the result is rounded once.
+    n, heads, page = 131072, 8, 1024
+    k = torch.zeros((n // page, heads, page, dim), dtype=dtype, device=DEV)
+    v = torch.ones_like(k)
+    k[0, :, 0], v[0, :, 0] = 1.0, 0.0
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV).repeat(reqs, 1)
+    q_begin = torch.arange(reqs + 1, dtype=torch.int32, device=DEV) * new
+    kv_len = torch.full((reqs,), n, dtype=torch.int32, device=DEV)
+    q = torch.ones((reqs * new, heads, dim), dtype=dtype, device=DEV)
+    out, lse, status = sz.paged_attention(q, k, v, table, q_begin, kv_len, scale=25.5 / dim * math.log(2), causal=False, return_lse=True)
+    assert not status.any()
+    mass = (n - 1) * 2.0 ** -25.5
+    want = mass / (1 + mass)
+    h = ref.HALF_STEP[dtype]
+    sums = (32 + n / 128) * 2.0 ** -24
+    tol = want * (2 * h + 2.0 ** -10 + sums + 2.0 ** -18) + (n * 2.0 ** -32 if dtype == FP16 else 0.0)
+    assert float((out.double() - want).abs().max()) <= tol
+    full = 25.5 * math.log(2) + math.log1p(mass)
+    assert float((lse.double() - full).abs().max()) <= sums + 2.0 ** -18 * full
+
+
 @pytest.mark.parametrize("layout", ["token_major", "one_pool", "rows_of_a_projection", "in_place"])
 @pytest.mark.parametrize("dim", [128, 40])
 def test_attention_layouts(layout, dim):
