@@ -559,8 +559,8 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *args, int32_
  * multiple of 8 tokens (of 128 above 128), at most 128 query heads share a KV
  * head and scale is positive; other shapes are computed key by key.
  * A device-side wait that runs out sets every status of the call to
- * SZ_ERR_DEVICE_TIMEOUT.  The workspace remembers the call: replays of a
- * captured call report it until the workspace is overwritten.
+ * SZ_ERR_DEVICE_TIMEOUT.  Replays of a captured call without a split row may
+ * report it for another ten seconds.
  */
 typedef struct sz_attention_args {
     const void *d_q;

@@ -250,12 +250,25 @@ struct TensorArgs {
     uint32_t ctas;
     float *parts;          // [ctas][2][kPartFloats]: the part that continues a block, the part that begins one
     SplitRec *rec;         // [ctas]
-    unsigned long long *timed_out;  // `call` once a wait of this call ran out
+    unsigned long long *timed_out;  // [2] once a wait of this call ran out: `call`, and the device time
     unsigned long long call;  // this call's tag, 48 bits
     int32_t *status;       // [n_reqs]
     uint64_t wait_limit_ns;
     uint32_t debug_flags;
 };
+
+// Whether a wait of this call ran out in another CTA.  Replays of a captured
+// call carry one tag, so what an earlier replay left there must go: the join
+// clears it, which runs once all CTAs are done; without a join it counts for
+// ten seconds (and a wait's limit), far longer than the CTAs of one launch lie
+// apart.
+constexpr int64_t kRecentNs = 10000000000;
+__device__ __forceinline__ bool timed_out(const TensorArgs &p) {
+    if (*(volatile unsigned long long *)p.timed_out != p.call) return false;
+    __threadfence();
+    const int64_t ago = (int64_t)(globaltimer_ns() - *(volatile unsigned long long *)(p.timed_out + 1));
+    return ago < kRecentNs || (uint64_t)(ago - kRecentNs) < p.wait_limit_ns;
+}
 
 // Visible keys of tokens [first, end) of a request: [*begin, *stop).
 __device__ __forceinline__ void key_range(const TensorArgs &p, const Request &q, int32_t first, int32_t end, int32_t *begin,
@@ -1248,7 +1261,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             if (lane == 0) {
                 p.status[r] = st;
                 __threadfence();  // a CTA that fails sets timed_out, then the statuses
-                if (*(volatile unsigned long long *)p.timed_out == p.call) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
+                if (timed_out(p)) p.status[r] = SZ_ERR_DEVICE_TIMEOUT;
             }
         }
     }
@@ -1278,6 +1291,8 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 mbar_wait(&bars.q_full[u % S::kQueries], u / S::kQueries & 1, patience);
         }
         if (tid == 0) {
+            *(volatile unsigned long long *)(p.timed_out + 1) = globaltimer_ns();
+            __threadfence();
             atomicExch(p.timed_out, p.call);
             __threadfence();
         }
@@ -1306,6 +1321,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
     __shared__ float shared[kJoinThreads][kChunks * 4 + 3];
     const uint32_t tid = threadIdx.x, c0 = blockIdx.x, chunk = blockIdx.y * kChunks, m_tile = blockIdx.z;
     grid_dependency_wait();
+    if (c0 == 0 && blockIdx.y == 0 && m_tile == 0 && tid == 0) *p.timed_out = 0;  // every CTA has looked
     const SplitRec w = p.rec[c0];
     if (w.last <= c0 || w.last >= p.ctas) return;
     const uint32_t first = (w.block * kM + m_tile) * p.tile_tokens;
@@ -1449,7 +1465,7 @@ static bool tensor_shape(const sz_paged_kv &kv, const sz_attention_args &a) {
 template <int D, int kM>
 static uint64_t tensor_workspace() {
     const uint64_t ctas = (uint64_t)kMaxTensorSms * Shape<D, kM>::kCtasPerSm;
-    return 8 + ctas * sizeof(SplitRec) + 2 * 4ull * Shape<D, kM>::kPartFloats * ctas;
+    return 16 + ctas * sizeof(SplitRec) + 2 * 4ull * Shape<D, kM>::kPartFloats * ctas;
 }
 
 // A tag for a call's words in the workspace: 48 bits, from a start of the
@@ -1498,7 +1514,7 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     const bool split = blocks > p.ctas || div_up((uint64_t)kv.max_pages * kv.page_tokens, p.key_tile) > kWholeTiles;
     const uint64_t most = div_up((uint64_t)kv.max_pages * kv.page_tokens, p.key_tile) + 1 + kBlockUnits<D, kM>;  // units of a block
     const bool wide = blocks >= (1ull << 32) / (p.ctas + 1) / most;  // units times CTAs may pass 32 bits
-    p.rec = split ? reinterpret_cast<SplitRec *>(at + 8) : nullptr;
+    p.rec = split ? reinterpret_cast<SplitRec *>(at + 16) : nullptr;
     p.call = next_call();
     p.status = status;
     p.wait_limit_ns = wait_limit_ns();

@@ -592,6 +592,49 @@ def test_the_output_is_encoded_behind_the_call():
         assert torch.equal(back.view(-1), want.view(torch.int16).view(-1))
 
 
+@pytest.mark.parametrize("new,kv,split", [([1, 2], [300, 70], False), ([1, 2], [3000, 70], True)])
+def test_a_timeout_does_not_stick_to_a_captured_call(new, kv, split):
+    # A call that ran into its limit leaves its tag and the time in the workspace
+    # (the only words of it that a call without split rows writes); the tag counts
+    # calls.  Given a captured call's tag there, its next replay reports it, and
+    # after the join, or if it is long ago, no later one does.
+    b = Batch(new, kv, 8, 2, 128, 16, BF16)
+    args = [b.q.to(DEV)] + b.cache()
+    ws = torch.zeros(sz.sz_plan_attention(128) // 8, dtype=torch.int64, device=DEV)
+    short = Batch([1], [20], 8, 2, 128, 16, BF16)
+    try:
+        sz.sz_debug_set_flags(1)
+        sz.sz_set_wait_limit_ns(2_000_000)
+        _, _, status = sz.paged_attention(short.q.to(DEV), *short.cache(), workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        sz.sz_debug_set_flags(0)
+        sz.sz_set_wait_limit_ns(1_000_000_000)
+    assert status.tolist() == [sz.SZ_ERR_DEVICE_TIMEOUT]
+    at = ws.nonzero().flatten().tolist()
+    assert len(at) == 2 and at[1] == at[0] + 1
+    mark = ws[at[0]:at[1] + 1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _, status = sz.paged_attention(*args, workspace=ws)
+
+    def replay(mark):
+        ws[at[0]:at[1] + 1] = mark
+        got = []
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            got.append(set(status.tolist()))
+        return got
+
+    now, ago = mark + torch.tensor([1, 0], device=DEV), mark + torch.tensor([1, -12_000_000_000], device=DEV)
+    late = {sz.SZ_ERR_DEVICE_TIMEOUT}
+    assert replay(mark) == [{0}, {0}]  # another call's
+    assert replay(now) == [late, {0} if split else late]
+    assert replay(ago) == [{0}, {0}]
+    assert torch.equal(out, sz.paged_attention(*args)[0])
+
+
 def test_two_captured_calls_share_a_workspace():
     b = Batch([1, 2], [3000, 700], 8, 2, 128, 16, BF16)
     c = Batch([200], [900], 8, 2, 128, 16, BF16, seed=9)
