@@ -63,8 +63,10 @@ void ints(const at::Tensor &t, const char *name, int64_t dims) {
         fail(PyExc_ValueError, "%s must be an int32 tensor of %d dimension(s) with entries side by side", name, (int)dims);
 }
 
+// Neither direction of differentiation goes through these operators.
 void no_gradient(const at::Tensor &t, const char *name) {
     if (t.requires_grad() && c10::GradMode::is_enabled()) fail(PyExc_ValueError, "%s requires a gradient, and this operator has none", name);
+    if (t._fw_grad(0).defined()) fail(PyExc_ValueError, "%s carries a tangent, and this operator has none", name);
 }
 
 // Rows [tokens, heads, dim]; returns the heads.
@@ -199,6 +201,7 @@ PyObject *append_kv(PyObject *const *a, Py_ssize_t n) {
     if (freqs) {
         if (freqs->scalar_type() != at::kDouble || freqs->dim() != 1 || !freqs->is_contiguous())
             fail(PyExc_ValueError, "rope_freqs must be a contiguous float64 vector");
+        no_gradient(*freqs, "rope_freqs");
         if (freqs->size(0) > 1 << 20) fail(PyExc_ValueError, "rope_freqs of %lld pairs", (long long)freqs->size(0));
         x.rot_dim = (uint32_t)(2 * freqs->size(0));
     }

@@ -16,7 +16,8 @@ Pages of a contiguous [page, head, token, channel] pool are pages of
 Both calls run on the current stream of the tensors' device, or on ``stream``
 (their new tensors are then allocated on it), never synchronise, and return a
 status tensor with one word per request.  Neither has a gradient: where
-gradients are recorded, tensors that require one are refused.
+gradients are recorded, tensors that require one are refused, and tensors that
+carry a tangent everywhere.
 """
 from __future__ import annotations
 

@@ -209,3 +209,20 @@ def test_gradients_are_refused_only_where_they_are_recorded():
         attend({**t, "k_pages": t["k_pages"].clone().requires_grad_()})
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # the next check
         put({**t, "k": t["k"].clone().requires_grad_()}, k_norm=w)
+
+
+def test_learned_frequencies_and_tangents_are_refused():
+    import torch.autograd.forward_ad as fwd
+    t = tensors()
+    with pytest.raises(ValueError, match="rope_freqs requires a gradient"):
+        put(t, rope_freqs=sz.rope_frequencies(64).requires_grad_())
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):  # the next check
+        put(t, rope_freqs=sz.rope_frequencies(64).requires_grad_())
+    with fwd.dual_level():
+        for name, call in (("q", attend), ("k_pages", attend), ("v_pages", put), ("k", put), ("v", put)):
+            dual = fwd.make_dual(t[name], torch.ones_like(t[name]))
+            with pytest.raises(ValueError, match=name + " carries a tangent"):
+                call({**t, name: dual})
+        w = torch.ones(t["q"].shape[2], dtype=t["q"].dtype)
+        with pytest.raises(ValueError, match="k_norm carries a tangent"):
+            put(t, k_norm=fwd.make_dual(w, w))
