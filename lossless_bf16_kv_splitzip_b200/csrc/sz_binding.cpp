@@ -69,6 +69,12 @@ void no_gradient(const at::Tensor &t, const char *name) {
     if (t._fw_grad(0).defined()) fail(PyExc_ValueError, "%s carries a tangent, and this operator has none", name);
 }
 
+// A tensor of the caller's that the call writes: whoever saved it for a
+// gradient finds out.  (Tensors of inference mode have no version.)
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Rows [tokens, heads, dim]; returns the heads.
 uint32_t rows(const at::Tensor &t, const char *name, at::ScalarType type, int64_t tokens, int64_t dim, uint64_t (&stride)[2]) {
     if (t.scalar_type() != type || t.dim() != 3 || t.size(0) != tokens || t.size(2) != dim)
@@ -245,6 +251,10 @@ PyObject *append_kv(PyObject *const *a, Py_ssize_t n) {
     x.d_positions_or_null = static_cast<const int64_t *>(at(positions));
     x.d_hists_or_null = static_cast<uint32_t *>(at(hists));
     x.d_hist_rows_or_null = static_cast<const uint32_t *>(at(hist_rows));
+    written(kp);
+    written(vp);
+    if (q_out) written(*q_out);
+    if (hists) written(*hists);
     x.interleaved = interleaved ? 1 : 0;
     x.rot_scale = (float)rot_scale;
     x.eps = (float)eps;
@@ -287,6 +297,7 @@ PyObject *paged_attention(PyObject *const *a, Py_ssize_t n) {
     if (with_lse) lse = at::empty({tokens, (int64_t)x.q_heads}, q.options().dtype(at::kFloat));
     const at::Tensor status = at::empty({(int64_t)kv.n_reqs}, kv_len.options());
     rows(out ? *out : made, "out", type, tokens, dim, x.out_stride);
+    if (out) written(*out);
     x.d_q = q.data_ptr();
     x.d_out = out ? out->data_ptr() : made.data_ptr();
     x.d_lse_or_null = with_lse ? static_cast<float *>(lse.data_ptr()) : nullptr;

@@ -850,6 +850,30 @@ def test_append_layouts_and_in_place(layout):
     assert torch.equal(k2.contiguous().view(torch.int16), k.view(torch.int16)) and torch.equal(v2.contiguous().view(torch.int16), v.view(torch.int16))
 
 
+def test_tensors_that_are_written_tell_so():
+    b = Batch([3, 1], [40, 20], 4, 2, 64, 16, BF16)
+    k, v, table, q_begin, kv_len = b.cache()
+    q, new = b.q.to(DEV), torch.randn(4, 2, 64, device=DEV).to(BF16)
+    q_out, out, hists = torch.empty_like(q), torch.empty_like(q), torch.zeros((4, 256), dtype=torch.int32, device=DEV)
+    read, put, got = (q, new, table, q_begin, kv_len), (k, v, q_out, hists), (out,)
+    was = [[t._version for t in g] for g in (read, put, got)]
+    sz.append_kv(new, new, k, v, table, q_begin, kv_len, q=q, q_out=q_out, hists=hists)
+    assert [t._version for t in put] == [n + 1 for n in was[1]]
+    sz.paged_attention(q_out, k, v, table, q_begin, kv_len, out=out)
+    assert [t._version for t in got] == [n + 1 for n in was[2]] and [t._version for t in put] == [n + 1 for n in was[1]]
+    assert [t._version for t in read] == was[0]
+    w = torch.ones(64, dtype=BF16, device=DEV, requires_grad=True)
+    y = (out * w).sum()  # `out` is saved
+    sz.paged_attention(q_out, k, v, table, q_begin, kv_len, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        k2, v2 = k.clone(), v.clone()
+        sz.append_kv(new, new, k2, v2, table, q_begin, kv_len)
+    _, status = sz.append_kv(new, new, k2, v2, table, q_begin, kv_len)  # and outside of it
+    assert not status.any() and torch.equal(k2.view(torch.int16), k.view(torch.int16))
+
+
 # --------------------------------------------------------------- together
 def test_prefill_transfer_and_continue():
     """A prefill in chunks writes the cache and counts it, the codec ships the
