@@ -57,11 +57,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB_PATH
 
 
+def binding_made_for() -> str:
+    """What a compiled binding fits: it reads torch's and Python's structures."""
+    import sysconfig
+
+    import torch
+    return "made for torch %s, python %s" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+
+
 def binding_is_stale() -> bool:
     if not os.path.exists(BINDING_PATH):
         return True
     t = os.path.getmtime(BINDING_PATH)
-    return any(os.path.getmtime(p) > t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "splitzip.h")))
+    if any(os.path.getmtime(p) > t for p in (BINDING_SOURCE, os.path.join(INCLUDE, "splitzip.h"))):
+        return True
+    with open(BINDING_PATH, "rb") as f:
+        return binding_made_for().encode() + b"\0" not in f.read()
 
 
 def build_binding(force: bool = False) -> str:
@@ -77,7 +88,7 @@ def build_binding(force: bool = False) -> str:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), '-DSZ_MADE_FOR="%s"' % binding_made_for()]
     cmd += ["-isystem" + d for d in dirs] + [BINDING_SOURCE, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING_PATH)

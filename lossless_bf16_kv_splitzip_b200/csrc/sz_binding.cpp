@@ -340,7 +340,9 @@ PyMethodDef methods[] = {
     {"paged_attention", (PyCFunction)(void *)entry<paged_attention>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// The module's docstring: what this file was compiled against, which the build
+// looks for in it.
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", SZ_MADE_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

@@ -226,3 +226,15 @@ def test_learned_frequencies_and_tangents_are_refused():
         w = torch.ones(t["q"].shape[2], dtype=t["q"].dtype)
         with pytest.raises(ValueError, match="k_norm carries a tangent"):
             put(t, k_norm=fwd.make_dual(w, w))
+
+
+def test_a_binding_of_another_torch_is_built_anew(monkeypatch):
+    from lossless_bf16_kv_splitzip_b200 import _build
+    sz.paged.binding()
+    assert not _build.binding_is_stale()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + "1")
+    assert _build.binding_is_stale()
+    monkeypatch.undo()
+    assert not _build.binding_is_stale()
+    monkeypatch.setattr("sysconfig.get_config_var", lambda name: "cpython-39")
+    assert _build.binding_is_stale()
