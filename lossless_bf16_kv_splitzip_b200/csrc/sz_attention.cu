@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kGeneralThreads) attention_any_kernel(sz_paged
             const Request q = load_request(kv, r);
             sz_status st = q.status;
             if (st == SZ_OK && q.n > 0 && q.kv > 0) {
-                const int32_t first = a.window ? max(0, q.kv - q.n - (int32_t)umin32(a.window, 0x7FFFFFFFu) + 1) : 0;
+                const int64_t first = a.window ? max((int64_t)0, (int64_t)q.kv - q.n - a.window + 1) : 0;
                 st = check_pages(kv, r, (uint32_t)first / kv.page_tokens, (uint32_t)(q.kv - 1) / kv.page_tokens + 1);
             }
             if ((tid & 31) == 0) status[r] = st;

@@ -462,6 +462,18 @@ def test_pages_behind_the_window_may_be_gone(dim):
 
 
 @pytest.mark.parametrize("dim", [128, 24])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1])
+def test_windows_wider_than_any_cache(dim, window):
+    # more new tokens than cached: the window begins before the cache, by more
+    # than 31 bits hold, and a bad page in it is found
+    b = Batch([9, 6], [4, 2], 4, 2, dim, 16, BF16)
+    attend_and_check(b, window=window)
+    b.table[1, 0] = 1 << 20
+    _, _, status = sz.paged_attention(b.q.to(DEV), *b.cache(), window=window)
+    assert status.tolist() == [0, sz.SZ_ERR_INVALID]
+
+
+@pytest.mark.parametrize("dim", [128, 24])
 def test_refused_requests(dim):
     b = Batch([2, 1, 1, 1, 1], [40, 40, 20, 33, 9], 4, 2, dim, 16, BF16)
     b.table[1, 1] = 1 << 30  # outside the pool
