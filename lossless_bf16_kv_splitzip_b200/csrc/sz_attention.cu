@@ -1452,12 +1452,13 @@ static cudaError_t allow_shared(uint32_t bytes) {
 }
 
 // Which shapes the tensor-core kernel takes: heads of 64 or 128 channels, a
-// positive scale (the running maximum is of unscaled scores), row tiles that
-// hold a whole group, and pages whose copies start on a swizzle group of 8
+// positive scale (the running maximum is of unscaled scores) whose products
+// with a score or with the difference of two neither vanish nor lose bits
+// before these overflow, row tiles that hold a whole group, and pages whose copies start on a swizzle group of 8
 // rows and fill or divide a tile.
 static bool tensor_shape(const sz_paged_kv &kv, const sz_attention_args &a) {
     if (kv.head_dim != 64 && kv.head_dim != 128) return false;
-    if (!(a.scale > 0.0f) || !(a.scale < 1e30f)) return false;
+    if (!(a.scale >= 1e-30f) || !(a.scale < 1e30f)) return false;
     if (a.q_heads / kv.heads > kTileRows || kv.n_pages == 0 || kv.n_tokens == 0) return false;
     return kv.page_tokens % 8 == 0 && (kv.page_tokens <= kTileRows || kv.page_tokens % kTileRows == 0);
 }
@@ -1497,7 +1498,6 @@ static cudaError_t launch_tensor(const sz_paged_kv &kv, const sz_attention_args 
     p.kv = kv;
     p.a = a;
     p.c = a.scale * kLog2e;
-    if (!(p.c > 1e-37f)) p.c = 1e-37f;  // a hidden score is -inf, and -inf * 0 would be NaN
     p.group = a.q_heads / kv.heads;
     p.tile_tokens = S::kRows / p.group;
     p.box_tokens = umin32(kv.page_tokens, kTileRows);

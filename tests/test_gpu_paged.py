@@ -164,6 +164,16 @@ def test_extreme_scores(dim):
     check(out[1:], hidden[0], hidden[2])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 72])
+@pytest.mark.parametrize("scale,size", [(3e-38, 5e17), (2e-30, 6e13), (-0.1, 1.0), (3e30, 2e-16)])
+def test_scales_of_any_size(dim, scale, size):
+    # queries and keys whose scores the scale brings back to ordinary numbers
+    b = Batch([3, 130], [200, 131], 4, 2, dim, 16, BF16)
+    b.q = (b.q.float() * size).to(BF16)
+    b.k = (b.k.float() * size).to(BF16)
+    attend_and_check(b, scale=scale)
+
+
 @pytest.mark.parametrize("dim", [128, 72])
 def test_infinite_and_nan_scores(dim):
     b = Batch([1, 1, 1, 1], [20, 200, 20, 20], 2, 1, dim, 16, BF16)
