@@ -557,7 +557,8 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *args, int32_
  * it either, whatever its bits.
  * Heads of 64 or 128 channels run on the tensor cores, if pages hold a
  * multiple of 8 tokens (of 128 above 128), at most 128 query heads share a KV
- * head and scale lies in [1e-30, 1e30); other calls are computed key by key.
+ * head, the queries' strides are head_dim at least and scale lies in [1e-30,
+ * 1e30); other calls are computed key by key.
  * A device-side wait that runs out sets every status of the call to
  * SZ_ERR_DEVICE_TIMEOUT.  Replays of a captured call without a split row may
  * report it for another ten seconds.

@@ -1454,12 +1454,15 @@ static cudaError_t allow_shared(uint32_t bytes) {
 // Which shapes the tensor-core kernel takes: heads of 64 or 128 channels, a
 // positive scale (the running maximum is of unscaled scores) whose products
 // with a score or with the difference of two neither vanish nor lose bits
-// before these overflow, row tiles that hold a whole group, and pages whose copies start on a swizzle group of 8
-// rows and fill or divide a tile.
+// before these overflow, row tiles that hold a whole group, and pages whose
+// copies start on a swizzle group of 8 rows and fill or divide a tile.
 static bool tensor_shape(const sz_paged_kv &kv, const sz_attention_args &a) {
     if (kv.head_dim != 64 && kv.head_dim != 128) return false;
     if (!(a.scale >= 1e-30f) || !(a.scale < 1e30f)) return false;
     if (a.q_heads / kv.heads > kTileRows || kv.n_pages == 0 || kv.n_tokens == 0) return false;
+    // queries repeated over heads or tokens, or lying over one another: a
+    // tensor map's rows do not overlap
+    if ((a.q_heads > 1 && a.q_stride[1] < kv.head_dim) || (kv.n_tokens > 1 && a.q_stride[0] < kv.head_dim)) return false;
     return kv.page_tokens % 8 == 0 && (kv.page_tokens <= kTileRows || kv.page_tokens % kTileRows == 0);
 }
 

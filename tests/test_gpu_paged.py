@@ -463,6 +463,35 @@ def test_attention_layouts(layout, dim):
         assert torch.equal(got[b.rows - 3:].cpu(), b.q[b.rows - 3:])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("repeat", ["heads", "tokens", "both", "overlap"])
+def test_rows_that_repeat(dim, repeat):
+    # queries, keys and values that are views with a stride of 0, or of less than a row
+    b = Batch([5, 60], [50, 131], 4, 2, dim, 16, BF16)
+    k, v, table, q_begin, kv_len = b.cache()
+    n = b.rows
+    base = torch.randn(n * dim + 4096, generator=b.g).to(BF16).to(DEV)
+
+    def rows(heads):
+        strides = {"heads": (dim, 0, 1), "tokens": (0, dim, 1), "both": (0, 0, 1), "overlap": (8, 16, 1)}[repeat]
+        return base.as_strided((n, heads, dim), strides)
+
+    q = rows(4)
+    out, _, status = sz.paged_attention(q, k, v, table, q_begin, kv_len)
+    assert not status.any()
+    want = ref.attention(q.cpu(), b.k, b.v, b.table, b.q_begin, b.kv_len, 1 / math.sqrt(dim))
+    check(out, want[0], want[2])
+    got = []
+    for new, q1 in ((rows(2), q), (rows(2).contiguous(), q.contiguous())):
+        k1, v1 = k.clone(), v.clone()
+        q_out, status = sz.append_kv(new, new, k1, v1, table, q_begin, kv_len, q=q1, rope_freqs=sz.rope_frequencies(dim // 16 * 16, device=DEV))
+        assert not status.any()
+        got.append([t.view(torch.int16) for t in (k1, v1, q_out)])
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    with pytest.raises(sz.SzError):  # written rows must lie apart
+        sz.paged_attention(q, k, v, table, q_begin, kv_len, out=rows(4))
+
+
 @pytest.mark.parametrize("dim", [128, 24])
 def test_pages_behind_the_window_may_be_gone(dim):
     b = Batch([1, 20], [300, 200], 4, 2, dim, 16, BF16)
