@@ -559,18 +559,16 @@ struct Watch {
     uint32_t failed, busy;
 };
 
-// Wait for a phase; false when the limit of device time ran out here or
-// elsewhere in the CTA.
+// Wait for a phase; false when the limit of device time ran out here (since
+// the last look that found no warp busy) or elsewhere in the CTA.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile Watch *watch, uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (watch->failed) return false;
-        if (globaltimer_ns() - t0 > limit_ns) {
-            if (watch->busy) {
-                t0 = globaltimer_ns();
-                continue;
-            }
+        const uint64_t now = globaltimer_ns();
+        if (watch->busy) t0 = now;
+        if (now - t0 > limit_ns) {
             watch->failed = 1u;
             return false;
         }
@@ -674,7 +672,10 @@ __device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32
     if (odd)
         for (int i = 0; i < D; i += 2) q_infinite |= not_finite<T>(*(const uint32_t *)(q + i)) != 0;
     const int32_t first = __reduce_min_sync(0xFFFFFFFFu, odd ? from : 0x7FFFFFFF), end = __reduce_max_sync(0xFFFFFFFFu, odd ? to : 0);
-    bool open = true;  // some row's NaN is not explained for good
+    uint32_t some = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) some |= nan[w];
+    bool open = __any_sync(0xFFFFFFFFu, some != 0) != 0;  // some row's NaN is not explained for good (infinities of both signs in its sum are none)
     for (int32_t j0 = first; open && j0 < end; j0 += 32) {
         const int32_t j = j0 + (int32_t)lane;
         const int32_t page = j < end ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
