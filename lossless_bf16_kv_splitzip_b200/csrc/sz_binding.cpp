@@ -65,6 +65,7 @@ void ints(const at::Tensor &t, const char *name, int64_t dims) {
 
 // Neither direction of differentiation goes through these operators.
 void no_gradient(const at::Tensor &t, const char *name) {
+    if (!t.unsafeGetTensorImpl()->autograd_meta()) return;
     if (t.requires_grad() && c10::GradMode::is_enabled()) fail(PyExc_ValueError, "%s requires a gradient, and this operator has none", name);
     if (t._fw_grad(0).defined()) fail(PyExc_ValueError, "%s carries a tangent, and this operator has none", name);
 }
