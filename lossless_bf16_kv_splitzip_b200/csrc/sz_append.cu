@@ -9,12 +9,14 @@
 // when pairs are adjacent -- so that turning needs no exchange between lanes.
 //
 // Bound: memory.  Every value is read once and written once, 4 bytes each:
-// 4,096 tokens of 32 + 8 + 8 heads of 128 with norms take 21.8 us, 4.6 TB/s
-// (70 % of a copy; 4 us of them a launch of little work takes as well), 4,096
-// of 64 + 8 + 8 heads 33.6 us, 5.0 TB/s (76 %), one token for each of 64
-// requests 4.5 us, which is latency.  With counts, 2,500 tokens on average of
-// 3 requests, 8 + 8 heads, 17.9 us: an atomic in shared memory per value
-// bounds it.
+// 4,096 tokens of 32 + 8 + 8 heads of 128 with norms take 22.6 us, 4.4 TB/s
+// (68 % of a copy; 4 us of them a launch of little work takes as well), 4,096
+// of 64 + 8 + 8 heads 33.7 us, 5.0 TB/s (76 %), one token for each of 64
+// requests 4.6 us, which is latency.  With counts, 2,052 tokens on average of
+// 3 requests, 8 + 8 heads, take 17.7 us, 2.8 TB/s: not the atomics, which the
+// histogram kernel issues at 4 us for as many values, but a warp that counts one
+// token before it loads its next, four such rounds in a row, and the clearing
+// and folding of 32 KB around them.
 // A warp takes one token and a run of its heads (D = 128: two heads at a
 // time, two 8-byte loads per lane), kBatch heads' loads under way per lane;
 // nothing but the counts needs other warps.  The first loads are issued before

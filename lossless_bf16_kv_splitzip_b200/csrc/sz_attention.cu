@@ -149,15 +149,22 @@ static cudaError_t launch_any_t(const sz_paged_kv &kv, const sz_attention_args &
 // P_X V.  While one row tile's softmax runs, the tensor cores work on the
 // other's products (kM = 2) or on the other CTA's of the SM (kM = 1).
 //
-// What bounds it: with few rows per request the reading of the keys and
-// values (64 requests of one token, 735 MB: 129 us, 5.7 TB/s, 87 % of a copy;
-// one token over 131,071 keys: 93 us, 5.8 TB/s); with many the products and,
-// beside them, the softmax's exponentials and conversions (4,096 tokens over
-// 32,768 keys, 32 heads of 128: 1.66 ms, 1,244 TFLOP/s, 74 % of the library's
-// matrix products in a burst, 89 % of their sustained rate); 3 us at the
-// start, in which a CTA finds its share, and 2 to 5 us a block for what does
-// not overlap -- queries, first scores, output -- bound short calls (one token
-// over 333 keys: 12 us).
+// What bounds it.  With few rows per request, the reading of the keys and
+// values: 64 requests of one token, 735 MB, 129 us in a replayed graph, 5.7
+// TB/s (87 % of a copy), 147 us as a call among others; one token over 131,071
+// keys 94 us, 5.7 TB/s, and 101.  With long chunks, the products and the
+// exponentials and conversions, neither alone: 4,096 tokens over 32,768 keys,
+// 32 heads of 128, keep the tensor cores busy for 68 % and the unit that does
+// the others for 69 % of the cycles, 1.66 ms in short runs (1,240 TFLOP/s, 74 %
+// of the library's matrix products in a burst), 1.91 ms call after call under
+// the power cap (1,080 TFLOP/s, 77 % of their sustained rate).  Behind a window
+// of 4,096 keys the same two stand at 57 and 58 %; the rest is what does not
+// overlap, 2 to 5 us a block: queries, first scores, output.  Ragged prompts
+// (64 channels) leave every unit idle for most of the time (tensor cores 20 %,
+// exponentials 38 %, memory 8 %): those block ends, key tiles that half of a
+// block's rows do not see, and unequal shares (the busiest SM's exponentials
+// stand at 53 %).  3 us at the start, in which a CTA finds its share, bound
+// short calls (one token over 333 keys: 12 us).
 //
 // The accumulator is rescaled only when a row's maximum has risen by more
 // than 2^8 since the reference that its weights were taken against: until
@@ -211,7 +218,8 @@ struct Shape {
     static constexpr uint32_t kStatusWarp = kM == 1 ? 7 : kMmaWarps == 2 ? kValueWarp : 9;
     static constexpr int kThreads = kM == 2 ? 384 : 256;
     // Registers a thread of the softmax and of the other warps (kM = 2): three
-    // warpgroups launched with 168 each, 2 * 208 + 88 = 3 * 168.
+    // warpgroups launched with 168 each, 2 * 208 + 88 = 3 * 168.  The compiler
+    // counts with 168 for all: the two-tile kernels spill 62 bytes.
     static constexpr int kManyRegs = 208, kFewRegs = 88;
     static constexpr int kCtasPerSm = kM == 2 ? 1 : 2;
     static constexpr uint32_t kColumns = kM == 2 ? 512 : 256;

@@ -3,9 +3,9 @@
 //
 // A decode step makes these calls once per layer.  With the checks and the
 // packing of the arguments in Python a call took the host 16.5 us (a single
-// token's append and its attention take the GPU 4.5 and 12 us); here it takes
-// 6.3 us for an append and 8 to 11 us for an attention of two launches, most
-// of which are the launches and the allocation of the results.  The C entry
+// token's append and its attention take the GPU 4.6 and 12 us); here it takes
+// 6.6 us for an append, 7.4 us for an attention of one launch and 11 us for one
+// of two, most of which are the launches and the allocation of the results.  The C entry
 // points are those of the library that the package has loaded (init), and
 // the errors that they return go back as their codes.
 #include <Python.h>
