@@ -105,10 +105,10 @@ __global__ void __launch_bounds__(kGeneralThreads) attention_any_kernel(sz_paged
     for (int g = 0; g < kGroups; ++g) mm = fmaxf(mm, part[g][kLanes * 8]);
     float ll = 0.0f, oo[8] = {};
     for (int g = 0; g < kGroups; ++g) {
-        const float lg = part[g][kLanes * 8 + 1];
-        if (lg == 0.0f) continue;  // a group without keys
-        const float f = exp2f(part[g][kLanes * 8] - mm);
-        ll += lg * f;
+        // a group whose keys all scored -inf (or without keys) has sums of 0, or
+        // NaN where such a key's value was not finite
+        const float mg = part[g][kLanes * 8], f = mg == -INFINITY ? 0.0f : exp2f(mg - mm);
+        ll += part[g][kLanes * 8 + 1] * f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) oo[i] += part[g][lane * 8 + i] * f;
     }
@@ -1217,13 +1217,13 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 for (int j = 0; j < 16; ++j) seen = add2(seen, pack2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1])));
             }
             const float2 seen2 = unpack2(seen);
-            const bool odd = mine && seen2.x + seen2.y != seen2.x + seen2.y && l > 0.0f && failed == 0;
+            const bool odd = mine && seen2.x + seen2.y != seen2.x + seen2.y && l == l && failed == 0;
             // where the output lies over the queries, neither of a pair may
             // write before both have read
             const bool wait_both = S::kPaired && whole && (const void *)p.a.d_out == p.a.d_q && pair_any(pair, odd);
             if (__any_sync(0xFFFFFFFFu, odd))
                 mend_rows<T, D, (int)kOwn>(&p, &control.watch, w.r, w.head, (const uint16_t *)p.a.d_q + (uint64_t)token * p.a.q_stride[0] + (uint64_t)head * p.a.q_stride[1],
-                                           odd, max(begin, w.t0 * (int32_t)p.key_tile), min(stop, w.t1 * (int32_t)p.key_tile), ref, o_at, half * kOwn);
+                                           odd, max(begin, w.t0 * (int32_t)p.key_tile), min(stop, w.t1 * (int32_t)p.key_tile), m == -INFINITY ? 0.0f : ref, o_at, half * kOwn);
             if (wait_both) pair_sync(pair);
             if (whole) {
 #pragma unroll
@@ -1364,8 +1364,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
             for (int e = 0; e < 4; ++e) o[j][e] *= keep;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (ml[i].y == 0.0f) continue;  // nothing visible there
-            const float f = exp2f(ml[i].x - top);
+            if (k0 + i * slices >= parts) continue;
+            // where nothing is visible, or all of it scored -inf, the part holds
+            // zeros, or NaN of a value that is not finite
+            const float f = ml[i].x == -INFINITY ? 0.0f : exp2f(ml[i].x - top);
             sum += ml[i].y * f;
 #pragma unroll
             for (int j = 0; j < kChunks; ++j) {
@@ -1387,8 +1389,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const __gr
             for (uint32_t k = 1; k < slices && k < parts; ++k) {
                 const float *const from = shared[k * row_span + row];
                 const float high = fmaxf(top, from[kChunks * 4]);
-                if (from[kChunks * 4 + 1] == 0.0f) continue;
-                const float keep = high == top ? 1.0f : exp2f(top - high), f = exp2f(from[kChunks * 4] - high);
+                const float keep = high == top ? 1.0f : exp2f(top - high), f = from[kChunks * 4] == -INFINITY ? 0.0f : exp2f(from[kChunks * 4] - high);
                 top = high;
                 sum = sum * keep + from[kChunks * 4 + 1] * f;
 #pragma unroll

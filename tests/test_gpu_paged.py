@@ -293,6 +293,42 @@ def test_values_that_are_not_finite_in_long_caches(case, new, kv, hq, hk, dim, d
     check(lse, wl, tl, "lse")
 
 
+@pytest.mark.parametrize("new,kv,dim", [(1, 9000, 128), (3, 9000, 64), (200, 5000, 64), (1, 60, 64), (150, 150, 128), (1, 60, 72), (20, 300, 40)])
+@pytest.mark.parametrize("first", [0, 2])
+def test_values_of_keys_that_score_minus_infinity(new, kv, dim, first):
+    # weight 0 exactly: 0 times a value that is not finite is NaN, wherever the
+    # key lies among those that are summed together, and where whole tiles score
+    # -inf; other channels are those of the other keys.  Rows that do not see it
+    # are clean (below, behind the window).
+    b = Batch([new], [kv], 2, 1, dim, 16, BF16, seed=43)
+    b.q = b.q.abs() + 0.1
+    bad = [first, first + 1, *range(kv // 2, kv // 2 + (300 if kv > 4000 else 1))]
+    for j in bad:
+        b.k[int(b.table[0, j // 16]), :, j % 16] = -math.inf
+    b.v[int(b.table[0, 0]), :, first + 1, 5] = math.inf
+    b.v[int(b.table[0, (kv // 2) // 16]), :, (kv // 2) % 16, 7] = math.nan
+    k, v, table, q_begin, kv_len = b.cache()
+    x = b.q.double().transpose(0, 1)
+    K, V = (ref.gather(t, b.table[0], kv)[:, 0].double() for t in (b.k, b.v))
+    K[bad], V[bad] = 0.0, 0.0
+    p, j = torch.arange(kv - new, kv)[:, None], torch.arange(kv)[None]
+    for window in (0, kv // 2 - 20):
+        out, lse, status = sz.paged_attention(b.q.to(DEV), k, v, table, q_begin, kv_len, window=window, return_lse=True)
+        assert not status.any()
+        out = out.double().cpu().transpose(0, 1)
+        inside = (j <= p) & ((j > p - window) if window else True)
+        seen = inside.clone()
+        seen[:, bad] = False
+        some = seen.any(1)
+        s = (x @ K.T / math.sqrt(dim)).masked_fill(~seen, -math.inf)
+        want = torch.softmax(s, -1) @ V
+        for channel, key in ((5, first + 1), (7, kv // 2)):
+            assert torch.equal(out[:, some, channel].isnan(), inside[some, key][None].expand(2, -1))
+            want[:, inside[:, key], channel] = out[:, inside[:, key], channel] = 0.0
+        assert float((out - want)[:, some].abs().max()) <= 2.0 ** -6 * float(V.abs().max())  # four half steps of the largest value
+        assert bool(out[:, ~some & inside.any(1)].isnan().any(-1).all())
+
+
 @pytest.mark.parametrize("new,hq", [(200, 1), (3, 4)])
 @pytest.mark.parametrize("dtype", [BF16, FP16])
 @pytest.mark.parametrize("over", [False, True])
