@@ -584,12 +584,11 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, vol
     return true;
 }
 // The roles whose accesses stay in bounds whatever the data go on after a
-// failure, which ends all further waits at once.  A copying warp asks this,
-// for all of its lanes, and stops: a phase may have been handed over unread,
-// its copies still under way.
+// failure, which ends all further waits at once; but the products' warp hands
+// nothing back that it has not seen land, so that no copy is issued over one
+// under way.  A copying warp asks this, for all of its lanes, and stops.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile Watch *watch, uint64_t limit_ns) {
-    const bool ok = wait_or_fail(bar, parity, watch, limit_ns);
-    return __all_sync(0xFFFFFFFFu, ok && watch->failed == 0) != 0;
+    return __all_sync(0xFFFFFFFFu, wait_or_fail(bar, parity, watch, limit_ns)) != 0;
 }
 
 // Columns outside [from, to) of a row's scores become -inf.
@@ -641,95 +640,84 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
 // over the keys that the row sees.  `o_at` holds channels [c0, c0 + kOwn).
 // Both are bound by the latency of a key's loads.  A chunk of 4,096 tokens over
 // 32,768 keys (32 heads of 128, 1.65 ms) takes no longer where all rows see an
-// infinity, 115 ms where a channel is infinite in every key, 160 ms where the
+// infinity, 94 ms where a channel is infinite in every key, 160 ms where the
 // last token's value is NaN and the two blocks per KV head that must not see it
 // are summed again.
 template <typename T, int D, int kOwn>
 __device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32_t r, uint32_t kv_head, const uint16_t *q, bool odd, int32_t from,
                                        int32_t to, float ref, uint32_t o_at, uint32_t c0) {
-    constexpr int kWords = kOwn / 32;  // a bit per channel
     const sz_paged_kv &kv = p->kv;
     const uint32_t lane = threadIdx.x & 31;
     if (lane == 0) atomicAdd(&watch->busy, 1u);
-    uint32_t nan[kWords], up[kWords] = {}, down[kWords] = {};
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-        uint32_t o[32];
-        tmem_ld32(o_at + w * 32, o);
-        tmem_wait_ld();
-        nan[w] = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (odd && __uint_as_float(o[i]) != __uint_as_float(o[i])) nan[w] |= 1u << i;
-    }
     const uint16_t *const keys = (const uint16_t *)kv.d_k + kv_head * kv.k_stride[1];
-    const uint16_t *const values = (const uint16_t *)kv.d_v + kv_head * kv.v_stride[1] + c0;
-    auto score = [&](const uint16_t *k) {
-        float s = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < D; i += 8) {
-            float a[8], b[8];
-            widen8<T>(*(const uint4 *)(q + i), a);
-            widen8<T>(*(const uint4 *)(k + i), b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += a[e] * b[e];
-        }
-        return s;
-    };
+    const uint16_t *values = (const uint16_t *)kv.d_v + kv_head * kv.v_stride[1] + c0;
     bool q_infinite = false;
     if (odd)
+#pragma unroll 1
         for (int i = 0; i < D; i += 2) q_infinite |= not_finite<T>(*(const uint32_t *)(q + i)) != 0;
-    const int32_t first = __reduce_min_sync(0xFFFFFFFFu, odd ? from : 0x7FFFFFFF), end = __reduce_max_sync(0xFFFFFFFFu, odd ? to : 0);
-    uint32_t some = 0;
+#pragma unroll 1
+    for (int w = 0; w < kOwn / 32; ++w, o_at += 32, values += 32) {  // 32 channels at a time, a bit each
+        uint32_t a[32];
+        tmem_ld32(o_at, a);
+        tmem_wait_ld();
+        uint32_t nan = 0, up = 0, down = 0;
 #pragma unroll
-    for (int w = 0; w < kWords; ++w) some |= nan[w];
-    bool open = __any_sync(0xFFFFFFFFu, some != 0) != 0;  // some row's NaN is not explained for good (infinities of both signs in its sum are none)
-    for (int32_t j0 = first; open && j0 < end; j0 += 32) {
-        const int32_t j = j0 + (int32_t)lane;
-        const int32_t page = j < end ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
-        const uint32_t slot = (uint32_t)j % kv.page_tokens;
-        uint32_t found = 0;
-        if (page >= 0) {
-            const uint16_t *const v = values + (uint64_t)page * kv.v_stride[0] + slot * kv.v_stride[2];
+        for (int i = 0; i < 32; ++i)
+            if (odd && __uint_as_float(a[i]) != __uint_as_float(a[i])) nan |= 1u << i;
+        bool open = __any_sync(0xFFFFFFFFu, nan != 0) != 0;  // some row's NaN is not explained for good
+        if (!open) continue;
+        const int32_t end = __reduce_max_sync(0xFFFFFFFFu, nan ? to : 0);
+#pragma unroll 1
+        for (int32_t j0 = __reduce_min_sync(0xFFFFFFFFu, nan ? from : 0x7FFFFFFF); open && j0 < end; j0 += 32) {
+            const int32_t j = j0 + (int32_t)lane;
+            const int32_t page = j < end ? page_of(kv, r, (uint32_t)j / kv.page_tokens) : -1;
+            const uint32_t slot = (uint32_t)j % kv.page_tokens;
+            uint32_t found = 0;
+            if (page >= 0) {
+                const uint16_t *const v = values + (uint64_t)page * kv.v_stride[0] + slot * kv.v_stride[2];
 #pragma unroll
-            for (int i = 0; i < kOwn / 8; ++i) {
-                const uint4 y = *(const uint4 *)(v + i * 8);
-                found |= not_finite<T>(y.x) | not_finite<T>(y.y) | not_finite<T>(y.z) | not_finite<T>(y.w);
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 y = *(const uint4 *)(v + i * 8);
+                    found |= not_finite<T>(y.x) | not_finite<T>(y.y) | not_finite<T>(y.z) | not_finite<T>(y.w);
+                }
             }
-        }
-        uint32_t hits = __ballot_sync(0xFFFFFFFFu, found != 0);
-        while (open && hits) {
-            const int src = __ffs(hits) - 1;
-            hits &= hits - 1;
-            const int32_t key = j0 + src;
-            const uint64_t key_page = (uint64_t)__shfl_sync(0xFFFFFFFFu, page, src), key_slot = __shfl_sync(0xFFFFFFFFu, slot, src);
-            const uint16_t *const v = values + key_page * kv.v_stride[0] + key_slot * kv.v_stride[2];
-            const bool sees = odd && key >= from && key < to;
-            // weight 0: a score of -inf, which finite numbers come to by
-            // overflow at most
-            const uint16_t *const k = keys + key_page * kv.k_stride[0] + key_slot * kv.k_stride[2];
-            bool infinite = q_infinite;
-            for (uint32_t i = 2 * lane; i < D; i += 64) infinite |= not_finite<T>(*(const uint32_t *)(k + i)) != 0;
-            const bool nothing = __any_sync(0xFFFFFFFFu, infinite) && sees && score(k) == -INFINITY;
-            bool more = false;
+            uint32_t hits = __ballot_sync(0xFFFFFFFFu, found != 0);
+#pragma unroll 1
+            while (open && hits) {
+                const int src = __ffs(hits) - 1;
+                hits &= hits - 1;
+                const uint64_t key_page = (uint64_t)__shfl_sync(0xFFFFFFFFu, page, src), key_slot = __shfl_sync(0xFFFFFFFFu, slot, src);
+                const uint32_t bits = (values + key_page * kv.v_stride[0] + key_slot * kv.v_stride[2])[lane];
+                const bool sees = odd && j0 + src >= from && j0 + src < to;
+                // weight 0: a score of -inf, which finite numbers come to by
+                // overflow at most
+                const uint16_t *const k = keys + key_page * kv.k_stride[0] + key_slot * kv.k_stride[2];
+                bool infinite = q_infinite;
+                for (uint32_t i = 2 * lane; i < D; i += 64) infinite |= not_finite<T>(*(const uint32_t *)(k + i)) != 0;
+                bool nothing = false;
+                if (__any_sync(0xFFFFFFFFu, infinite) && sees) {
+                    float s = 0.0f;
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 8) {
+                        float x[8], y[8];
+                        widen8<T>(*(const uint4 *)(q + i), x);
+                        widen8<T>(*(const uint4 *)(k + i), y);
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                const uint32_t bits = v[w * 32 + lane];
+                        for (int e = 0; e < 8; ++e) s += x[e] * y[e];
+                    }
+                    nothing = s == -INFINITY;
+                }
                 const float y = Half2<T>::widen(bits).x;
                 const bool any = not_finite<T>(bits) != 0;
                 const uint32_t up1 = __ballot_sync(0xFFFFFFFFu, any && !(y < 0.0f)), down1 = __ballot_sync(0xFFFFFFFFu, any && !(y > 0.0f));
                 if (sees) {
-                    up[w] |= nothing ? up1 | down1 : up1;
-                    down[w] |= nothing ? up1 | down1 : down1;
+                    up |= nothing ? up1 | down1 : up1;
+                    down |= nothing ? up1 | down1 : down1;
                 }
-                more |= (nan[w] & ~(up[w] & down[w])) != 0;
+                open = __any_sync(0xFFFFFFFFu, (nan & ~(up & down)) != 0) != 0;
             }
-            open = __any_sync(0xFFFFFFFFu, more) != 0;
         }
-    }
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-        const uint32_t lost = nan[w] & ~(up[w] | down[w]);
+        const uint32_t lost = nan & ~(up | down);
         float o[32] = {};
         const int32_t end1 = __reduce_max_sync(0xFFFFFFFFu, lost ? to : 0);
 #pragma unroll 1
@@ -740,7 +728,7 @@ __device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32
             // keys without a page: the pool's first, with weight 0
             const uint64_t page1 = page >= 0 ? (uint32_t)page : 0, slot = page >= 0 ? (uint32_t)j % kv.page_tokens : 0;
             const uint64_t k_at = (uint64_t)(keys + page1 * kv.k_stride[0] + slot * kv.k_stride[2]);
-            const uint64_t v_at = (uint64_t)(values + page1 * kv.v_stride[0] + slot * kv.v_stride[2] + w * 32);
+            const uint64_t v_at = (uint64_t)(values + page1 * kv.v_stride[0] + slot * kv.v_stride[2]);
 #pragma unroll 1
             for (int t = 0; t < 32; t += 2) {
                 // two keys at a time, which share the loads of q; those after next are on their way to the first cache
@@ -755,14 +743,14 @@ __device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32
                 float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 8) {
-                    float a[8], b[8];
-                    widen8<T>(*(const uint4 *)(q + i), a);
-                    widen8<T>(*(const uint4 *)(k0 + i), b);
+                    float x[8], y[8];
+                    widen8<T>(*(const uint4 *)(q + i), x);
+                    widen8<T>(*(const uint4 *)(k0 + i), y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s0 += a[e] * b[e];
-                    widen8<T>(*(const uint4 *)(k1 + i), b);
+                    for (int e = 0; e < 8; ++e) s0 += x[e] * y[e];
+                    widen8<T>(*(const uint4 *)(k1 + i), y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s1 += a[e] * b[e];
+                    for (int e = 0; e < 8; ++e) s1 += x[e] * y[e];
                 }
                 const float e0 = exp2f(fmaf(s0, p->c, -ref)), e1 = exp2f(fmaf(s1, p->c, -ref));
 #pragma unroll
@@ -782,16 +770,16 @@ __device__ __noinline__ void mend_rows(const TensorArgs *p, Watch *watch, uint32
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t a[16];
-            tmem_ld16(o_at + w * 32 + h * 16, a);
+            uint32_t b[16];
+            tmem_ld16(o_at + h * 16, b);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const uint32_t bit = 1u << (h * 16 + i);
-                if (lost & bit) a[i] = __float_as_uint(o[h * 16 + i]);
-                if (nan[w] & (up[w] ^ down[w]) & bit) a[i] = up[w] & bit ? 0x7F800000u : 0xFF800000u;
+                if (lost & bit) b[i] = __float_as_uint(o[h * 16 + i]);
+                if (nan & (up ^ down) & bit) b[i] = up & bit ? 0x7F800000u : 0xFF800000u;
             }
-            tmem_st16(o_at + w * 32 + h * 16, a);
+            tmem_st16(o_at + h * 16, b);
         }
     }
     tmem_wait_st();
@@ -985,6 +973,7 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
             if (++slot == S::kSlots) slot = 0, phase ^= 1;
         };
         const uint32_t mine = wid - kMmaWarp;
+        bool landed = true;            // every copy waited for so far
         auto each = [&](auto f) {  // row tile of this warp's
             if constexpr (S::kMmaWarps == 2) {
                 f(mine);
@@ -1010,22 +999,22 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                 }
                 __syncwarp();
             };
-            wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, watch, limit);
-            wait_or_fail(&bars.full[slot], phase, watch, limit);
+            landed &= wait_or_fail(&bars.q_full[buf], piece / S::kQueries & 1, watch, limit);
+            landed &= wait_or_fail(&bars.full[slot], phase, watch, limit);
             tc_fence_after();
             each([&](uint32_t m) {
                 if (m < tiles) score(m);
             });
-            if (one) mma_commit(&bars.empty[slot]);
+            if (one && landed) mma_commit(&bars.empty[slot]);
             pass();
             for (int32_t t = t_begin; t < t_end; ++t) {
                 const uint32_t v_slot = slot;
                 const bool more = t + 1 < t_end;
-                wait_or_fail(&bars.full[slot], phase, watch, limit);
+                landed &= wait_or_fail(&bars.full[slot], phase, watch, limit);
                 pass();
                 if (more)  // the next K now, so that nothing is waited for between the products
-                    wait_or_fail(&bars.full[slot], phase, watch, limit);
-                else if (one)
+                    landed &= wait_or_fail(&bars.full[slot], phase, watch, limit);
+                else if (one && landed)
                     mma_commit(&bars.q_empty[buf]);
                 // keys behind the last token in this tile's last page: their
                 // weights are 0, so their values must be finite
@@ -1059,11 +1048,11 @@ attention_kernel(const __grid_constant__ TensorArgs p, const __grid_constant__ C
                             __syncwarp();
                         }
                     }
-                    if (one && (S::kMmaWarps == 2 || m + 1 == kM)) mma_commit(&bars.empty[v_slot]);
+                    if (one && landed && (S::kMmaWarps == 2 || m + 1 == kM)) mma_commit(&bars.empty[v_slot]);
                     if (more && m < tiles) score(m);
                 });
                 if (S::kMmaWarps == 2) done += mine < tiles ? 1 : 0; else ++done, done2 += tiles > 1 ? 1 : 0;
-                if (more && one) mma_commit(&bars.empty[slot]);
+                if (more && one && landed) mma_commit(&bars.empty[slot]);
                 if (more) pass();
             }
         }
