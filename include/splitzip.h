@@ -554,7 +554,8 @@ sz_status sz_append_kv(const sz_paged_kv *kv, const sz_append_args *args, int32_
  * the weights exp(s - m) are rounded to the 16-bit type before they meet the
  * values.  The result does not depend on timing: parts of a split row are
  * joined in a fixed order.  A key or value hidden from a query does not reach
- * it either, whatever its bits.
+ * it either, whatever its bits; an infinity or NaN among the values that it
+ * sees does, however small the weight.
  * Heads of 64 or 128 channels run on the tensor cores, if pages hold a
  * multiple of 8 tokens (of 128 above 128), at most 128 query heads share a KV
  * head, the queries' strides are head_dim at least and scale lies in [1e-30,
